@@ -1,0 +1,151 @@
+"""The operators around the linear layer (include/instant_ops.h), without a GPU: the boundary is
+exported, and what a call may not be is refused on the host before anything is enqueued."""
+import ctypes
+import os
+import re
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "instant_ops.h")
+
+import rank_compressed_backprop_amd as rcb  # noqa: E402
+from rank_compressed_backprop_amd import ops  # noqa: E402
+
+A, W = 0x1000, 0x2000  # pointers that are never read: every call here is refused, or has no rows
+E_ARG, E_SHAPE, OK = rcb.INSTANT_E_ARG, rcb.INSTANT_E_SHAPE, rcb.INSTANT_OK
+BF, FP = rcb.INSTANT_BF16, rcb.INSTANT_FP32
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return set(re.findall(r"\b(instant_[a-z_]+)\s*\(", text))
+
+
+def test_boundary_is_exported():
+    assert declared() == set(ops.EXPORTED)
+    lib = ctypes.CDLL(rcb.LIB_PATH)
+    for name in declared():
+        assert hasattr(lib, name), name
+
+
+def test_workspace_sizes():
+    for bad in [(-1, 8, 8, BF), (4, 0, 8, BF), (4, 8, -8, BF), (4, 12, 8, BF), (4, 8, 20, BF), (4, 8, 8, 2),
+                (1 + (1 << 26), 8, 8, BF), (4, 8 + (1 << 18), 8, BF)]:
+        assert ops.instant_linear_workspace_bytes(*bad) == 0, bad
+    for bad in [(-1, 8), (4, 0), (4, 12), (4, 65544)]:
+        assert ops.instant_rmsnorm_workspace_bytes(*bad) == 0, bad
+    for M in (0, 1, 7, 1 << 20, 1 << 26):
+        for dt in (BF, FP):
+            n = ops.instant_linear_workspace_bytes(M, 4096, 1024, dt)
+            assert n >= 256 and n % 256 == 0
+            assert n < 1 << 31  # the partial sums' size does not grow with the batch
+        n = ops.instant_rmsnorm_workspace_bytes(M, 65536)
+        assert n >= 256 and n % 256 == 0
+
+
+def fwd(x=A, w=A, bias=None, res=None, M=4, N=64, K=64, dtype=BF, act=0, y=A, z=None, zq=None, zs=None, ws=W,
+        n=1 << 30):
+    return ops.instant_linear_fwd(x, w, bias, res, M, N, K, dtype, act, y, z, zq, zs, ws, n, 0)
+
+
+def test_linear_fwd_refusals():
+    for change in [dict(x=None), dict(w=None), dict(y=None), dict(x=A + 8), dict(w=A + 2), dict(bias=A + 4),
+                   dict(res=A + 8), dict(y=A + 8), dict(z=A + 8), dict(zq=A + 8, zs=A), dict(zq=A), dict(zs=A),
+                   dict(z=A, zq=A, zs=A), dict(M=-1), dict(N=0), dict(K=-8), dict(dtype=2), dict(act=5),
+                   dict(act=-1)]:
+        assert fwd(**change) == E_ARG, change
+    for change in [dict(N=60), dict(K=68)]:
+        assert fwd(**change) == E_SHAPE, change
+    assert fwd(M=0, x=None, w=None, y=None, ws=None, n=0) == OK
+    # a workspace that the sizes need: absent, misaligned, too small
+    big = dict(M=8, N=64, K=8192)
+    assert ops.instant_linear_workspace_bytes(8, 64, 8192, FP) > 256
+    assert fwd(**big, dtype=FP, ws=None) == E_ARG
+    assert fwd(**big, dtype=FP, ws=W + 128) == E_ARG
+    assert fwd(**big, dtype=FP, n=64) == E_SHAPE
+
+
+def act_bwd(gy=A, z=A, zq=None, zs=None, M=4, N=64, dtype=BF, act=2, gz=A, gb=None, ws=W, n=1 << 30):
+    return ops.instant_act_bwd(gy, z, zq, zs, M, N, dtype, act, gz, gb, ws, n, 0)
+
+
+def test_act_bwd_refusals():
+    for change in [dict(gy=None), dict(z=None), dict(z=A, zq=A, zs=A), dict(z=None, zq=A), dict(z=None, zs=A),
+                   dict(gz=None), dict(act=0), dict(act=0, z=None, zq=A, zs=A), dict(gy=A + 8), dict(z=A + 8),
+                   dict(gz=A + 8), dict(gb=A + 8), dict(M=-1), dict(N=0), dict(dtype=7), dict(act=9),
+                   dict(gb=A, ws=None), dict(gb=A, ws=W + 8)]:
+        assert act_bwd(**change) == E_ARG, change
+    assert act_bwd(N=12) == E_SHAPE
+    assert act_bwd(gb=A, n=16) == E_SHAPE
+    assert act_bwd(M=0, gy=None, z=None) == OK
+
+
+def bwd(gz=A, w=A, x=A, xq=None, xs=None, M=4, N=64, K=64, dtype=BF, gx=A, gw=A, ws=W, n=1 << 30):
+    return ops.instant_linear_bwd(gz, w, x, xq, xs, M, N, K, dtype, gx, gw, ws, n, 0)
+
+
+def test_linear_bwd_refusals():
+    for change in [dict(gz=None), dict(w=None), dict(x=None), dict(xq=A, xs=A), dict(x=None, xq=A),
+                   dict(x=None, xs=A), dict(gx=None, gw=None), dict(gz=A + 8), dict(w=A + 8), dict(x=A + 8),
+                   dict(gx=A + 8), dict(gw=A + 8), dict(x=None, xq=A + 8, xs=A), dict(M=-2), dict(N=0), dict(K=0),
+                   dict(dtype=-1)]:
+        assert bwd(**change) == E_ARG, change
+    for change in [dict(N=4), dict(K=100)]:
+        assert bwd(**change) == E_SHAPE, change
+    assert bwd(M=0, gz=None, w=None, x=None, gw=None, ws=None, n=0) == OK  # no rows: gx has none
+    big = dict(M=8192, N=8, K=8)
+    assert bwd(**big, dtype=FP, ws=None) == E_ARG
+    assert bwd(**big, dtype=FP, n=0) == E_SHAPE
+
+
+def test_ckpt_refusals():
+    for change in [dict(x=None), dict(q=None), dict(s=None), dict(x=A + 8), dict(q=A + 8), dict(M=-1), dict(C=0),
+                   dict(dtype=5)]:
+        a = dict(x=A, M=4, C=64, dtype=BF, q=A, s=A) | change
+        assert ops.instant_ckpt_pack(a["x"], a["M"], a["C"], a["dtype"], a["q"], a["s"], 0) == E_ARG, change
+        assert ops.instant_ckpt_unpack(a["q"], a["s"], a["M"], a["C"], a["dtype"], a["x"], 0) == E_ARG, change
+    assert ops.instant_ckpt_pack(A, 4, 36, BF, A, A, 0) == E_SHAPE
+    assert ops.instant_ckpt_unpack(A, A, 4, 36, BF, A, 0) == E_SHAPE
+    assert ops.instant_ckpt_pack(None, 0, 64, BF, None, None, 0) == OK
+    assert ops.instant_ckpt_unpack(None, None, 0, 64, BF, None, 0) == OK
+
+
+def test_rmsnorm_refusals():
+    def nf(x=A, res=None, g=A, M=4, C=64, dtype=BF, eps=1e-5, h=None, y=A, yq=None, ys=None, rstd=A):
+        return ops.instant_rmsnorm_fwd(x, res, g, M, C, dtype, eps, h, y, yq, ys, rstd, 0)
+    for change in [dict(x=None), dict(g=None), dict(res=A), dict(h=A), dict(y=None), dict(yq=A), dict(ys=A),
+                   dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x=A + 8), dict(g=A + 8),
+                   dict(y=A + 8), dict(rstd=A + 2), dict(M=-1), dict(C=0), dict(dtype=3), dict(res=A + 8, h=A)]:
+        assert nf(**change) == E_ARG, change
+    assert nf(C=20) == E_SHAPE and nf(C=65544) == E_SHAPE
+    assert nf(M=0) == OK
+
+    def nb(gy=A, h=A, g=A, rstd=A, gh=None, M=4, C=64, dtype=BF, gx=A, gg=A, ws=W, n=1 << 30):
+        return ops.instant_rmsnorm_bwd(gy, h, g, rstd, gh, M, C, dtype, gx, gg, ws, n, 0)
+    for change in [dict(gy=None), dict(h=None), dict(g=None), dict(rstd=None), dict(gx=None), dict(gy=A + 8),
+                   dict(h=A + 8), dict(gh=A + 8), dict(gx=A + 8), dict(gg=A + 8), dict(rstd=A + 1), dict(M=-1),
+                   dict(C=0), dict(dtype=3), dict(ws=None), dict(ws=W + 16)]:
+        assert nb(**change) == E_ARG, change
+    assert nb(C=20) == E_SHAPE and nb(C=65544) == E_SHAPE and nb(n=8) == E_SHAPE
+    assert nb(M=0, gg=None) == OK
+
+
+def test_tensor_functions_refuse_cpu_tensors_and_bad_shapes():
+    """Shapes and types are checked before the device, so no GPU is asked."""
+    x = torch.zeros(4, 12)
+    with pytest.raises(TypeError):
+        ops.checkpoint_pack(torch.zeros(4, 16, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        ops.checkpoint_pack(torch.tensor(1.0))
+    with pytest.raises(ValueError):
+        ops.checkpoint_pack(torch.zeros(16, 4).t())
+    for call in (lambda: ops.checkpoint_pack(x), lambda: ops.linear_forward(x, x),
+                 lambda: ops.rmsnorm_forward(x, x[0]), lambda: ops.activation_backward(x, x),
+                 lambda: ops.checkpoint_pack(torch.zeros(4, 16))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ops.checkpoint_unpack(ops.Checkpoint8(x, x), torch.float16)
