@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "ops.hpp"
+#include "tile16.hpp"
 
 namespace instant {
 
@@ -186,6 +187,14 @@ int slices32(int a, int b, int K) {
   return S;
 }
 
+template <class T>
+hipError_t sum_parts(const float* part, int S, int M, int N, const Epi& ep, hipStream_t st) {
+  const size_t units = (size_t)M * ck_groups(N) * 4;
+  hipLaunchKernelGGL((part_sum_kernel<T>), dim3((unsigned)std::min<size_t>((units + 255) / 256, 4096)), dim3(256), 0,
+                     st, part, S, M, N, ep);
+  return hipGetLastError();
+}
+
 template <class T, int ASRC, int BSRC>
 hipError_t run32(const Operand& a, const Operand& b, int K, const Epi& ep, float* part, hipStream_t st) {
   const int S = slices32(a.rows, b.rows, K);
@@ -198,47 +207,65 @@ hipError_t run32(const Operand& a, const Operand& b, int K, const Epi& ep, float
   hipLaunchKernelGGL((tile32_kernel<T, ASRC, BSRC, true>), dim3(tiles, 1, S), dim3(256), 0, st, a, b, K, ep, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t units = (size_t)a.rows * ck_groups(b.rows) * 4;
-  hipLaunchKernelGGL((part_sum_kernel<T>), dim3((unsigned)std::min<size_t>((units + 255) / 256, 4096)), dim3(256), 0,
-                     st, (const float*)part, S, a.rows, b.rows, ep);
-  return hipGetLastError();
+  return sum_parts<T>(part, S, a.rows, b.rows, ep, st);
 }
+
+// float32 words of the bfloat16 copy that a checkpoint of x is unpacked to for gw
+size_t gw_unpacked_floats(int M, int K) { return ((size_t)M * K / 2 + 63) / 64 * 64; }
 
 Epi plain_out(void* out) { return Epi{nullptr, nullptr, out, nullptr, Ckpt{nullptr, nullptr}, ACT_NONE}; }
 
 }  // namespace
 
+namespace {
+
+hipError_t run16(bool akm, bool bkm, const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep,
+                 float* part, hipStream_t st) {
+  const int S = plan16(M, N, K).S;
+  if (S > 1 && !part) return hipErrorInvalidValue;
+  const hipError_t e = launch_tile16(akm, bkm, A, lda, M, B, ldb, N, K, ep, part, st);
+  return e == hipSuccess && S > 1 ? sum_parts<bf16>(part, S, M, N, ep, st) : e;
+}
+
+}  // namespace
+
 size_t linear_part_floats(bool bf16_io, Prod p, int M, int N, int K) {
-  (void)bf16_io;
   const int a = p == Prod::Gw ? N : M, b = p == Prod::Fwd ? N : K, k = p == Prod::Fwd ? K : p == Prod::Gx ? N : M;
   if (!a || !k) return 0;
-  const int S = slices32(a, b, k);
-  return S > 1 ? (size_t)S * a * b : 0;
+  const int S = bf16_io ? plan16(a, b, k).S : slices32(a, b, k);
+  return (S > 1 ? (size_t)S * a * b : 0) + (bf16_io && p == Prod::Gw ? gw_unpacked_floats(M, K) : 0);
 }
 
 hipError_t launch_linear_fwd(bool bf16_io, const void* x, const void* w, int M, int N, int K, const Epi& ep,
                              float* part, hipStream_t st) {
+  if (bf16_io) return run16(false, false, x, K, M, w, K, N, K, ep, part, st);
   const Operand a{x, nullptr, K, M}, b{w, nullptr, K, N};
-  return bf16_io ? run32<bf16, SRC_ROWK, SRC_ROWK>(a, b, K, ep, part, st)
-                 : run32<float, SRC_ROWK, SRC_ROWK>(a, b, K, ep, part, st);
+  return run32<float, SRC_ROWK, SRC_ROWK>(a, b, K, ep, part, st);
 }
 
 hipError_t launch_linear_gx(bool bf16_io, const void* gz, const void* w, int M, int N, int K, void* gx, float* part,
                             hipStream_t st) {
+  if (bf16_io) return run16(false, true, gz, N, M, w, K, K, N, plain_out(gx), part, st);
   const Operand a{gz, nullptr, N, M}, b{w, nullptr, K, K};
-  return bf16_io ? run32<bf16, SRC_ROWK, SRC_KMAJ>(a, b, N, plain_out(gx), part, st)
-                 : run32<float, SRC_ROWK, SRC_KMAJ>(a, b, N, plain_out(gx), part, st);
+  return run32<float, SRC_ROWK, SRC_KMAJ>(a, b, N, plain_out(gx), part, st);
 }
 
 hipError_t launch_linear_gw(bool bf16_io, const void* gz, const void* x, Ckpt xc, int M, int N, int K, void* gw,
                             float* part, hipStream_t st) {
-  const Operand a{gz, nullptr, N, N}, b{xc.q ? (const void*)xc.q : x, xc.scale, K, K};
   const Epi ep = plain_out(gw);
-  if (xc.q)
-    return bf16_io ? run32<bf16, SRC_KMAJ, SRC_KMAJ_Q8>(a, b, M, ep, part, st)
-                   : run32<float, SRC_KMAJ, SRC_KMAJ_Q8>(a, b, M, ep, part, st);
-  return bf16_io ? run32<bf16, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st)
-                 : run32<float, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st);
+  if (bf16_io && M > 0) {  // (no rows: zeros, from the kernel below)
+    if (xc.q) {
+      const hipError_t e = launch_ckpt_unpack(true, xc, M, K, part, st);
+      if (e != hipSuccess) return e;
+      x = part;
+      part += gw_unpacked_floats(M, K);
+    }
+    return run16(true, true, gz, N, N, x, K, K, M, ep, part, st);
+  }
+  const Operand a{gz, nullptr, N, N}, b{xc.q ? (const void*)xc.q : x, xc.scale, K, K};
+  if (bf16_io) return run32<bf16, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st);
+  if (xc.q) return run32<float, SRC_KMAJ, SRC_KMAJ_Q8>(a, b, M, ep, part, st);
+  return run32<float, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st);
 }
 
 }  // namespace instant
