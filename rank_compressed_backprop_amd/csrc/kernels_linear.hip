@@ -210,8 +210,12 @@ hipError_t run32(const Operand& a, const Operand& b, int K, const Epi& ep, float
   return sum_parts<T>(part, S, a.rows, b.rows, ep, st);
 }
 
-// float32 words of the bfloat16 copy that a checkpoint of x is unpacked to for gw
-size_t gw_unpacked_floats(int M, int K) { return ((size_t)M * K / 2 + 63) / 64 * 64; }
+// float32 words of the bfloat16 copy that a checkpoint of x is unpacked to for gw; 0 where that
+// would take more than 1 GB (the float32-arithmetic kernel then reads the checkpoint itself)
+size_t gw_unpacked_floats(int M, int K) {
+  const size_t n = ((size_t)M * K / 2 + 63) / 64 * 64;
+  return n > ((size_t)1 << 28) ? 0 : n;
+}
 
 Epi plain_out(void* out) { return Epi{nullptr, nullptr, out, nullptr, Ckpt{nullptr, nullptr}, ACT_NONE}; }
 
@@ -219,33 +223,76 @@ Epi plain_out(void* out) { return Epi{nullptr, nullptr, out, nullptr, Ckpt{nullp
 
 namespace {
 
-hipError_t run16(bool akm, bool bkm, const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep,
+template <class L>
+hipError_t run16(L launch, const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep,
                  float* part, hipStream_t st) {
   const int S = plan16(M, N, K).S;
   if (S > 1 && !part) return hipErrorInvalidValue;
-  const hipError_t e = launch_tile16(akm, bkm, A, lda, M, B, ldb, N, K, ep, part, st);
+  const hipError_t e = launch(A, lda, M, B, ldb, N, K, ep, part, st);
   return e == hipSuccess && S > 1 ? sum_parts<bf16>(part, S, M, N, ep, st) : e;
 }
 
 }  // namespace
 
+// A product's time by what its blocks cost: a compute unit runs `fit` blocks of a shape at once;
+// a block takes at least `lone` us a stage (the latency of its requests), k of them together at
+// least k * `each` (the matrix cores and the operands' way to them), and `ends` for its start and
+// its epilogue. Split K pays for a second launch and the partials' way to memory and back. The
+// figures are fitted to the times of 39 products of 1 to 16384 rows by 10 tile shapes and ring
+// depths by 10 splits on gfx950 (13% rms); the shape chosen is within 5% of the best one measured
+// in 31 of the 39, at worst 18% off (4.6 against 3.9 us). Examples, best against a fixed 256 x
+// 256 tile: 8 x 11008 over 4096 15.0 against 73 us, 768 x 768 over 16384 39.6 against 309 us,
+// 512 x 4096 over 1024 8.8 against 31 us.
+Plan16 plan16(int M, int N, int K) {
+  struct Shape {
+    int wm, wn, ns, fit;
+    float lone, each, ends;
+  };
+  static constexpr Shape shapes[] = {
+      {8, 8, 2, 1, 1.24f, 1.24f, 8.1f}, {8, 6, 2, 1, 0.91f, 0.87f, 6.3f}, {4, 4, 2, 2, 0.56f, 0.43f, 2.4f},
+      {4, 4, 4, 1, 0.42f, 0.25f, 3.5f}, {2, 4, 3, 2, 0.30f, 0.27f, 2.0f}, {2, 4, 2, 3, 0.47f, 0.28f, 1.6f},
+      {2, 2, 2, 4, 0.42f, 0.17f, 1.1f}, {2, 2, 4, 2, 0.13f, 0.18f, 1.45f}};
+  static constexpr int slices[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int nst = (K + 63) / 64;
+  Plan16 best{0, 0, 0, 1};
+  float least = 0.0f;
+  for (const Shape& s : shapes) {
+    const long tiles = (((long)M + 32 * s.wm - 1) / (32 * s.wm)) * (((long)N + 32 * s.wn - 1) / (32 * s.wn));
+    for (int S : slices) {
+      if (S > 1 && (tiles * S > 2048 || nst < 2 * S)) break;
+      const long n = (tiles * S + 255) / 256;  // blocks of the busiest compute unit
+      const int nq = (nst + S - 1) / S;
+      auto group = [&](int k) { return nq * std::max(s.lone, k * s.each) + s.ends * (0.5f + 0.5f * k); };
+      const int rest = (int)(n % s.fit);
+      float t = (float)(n / s.fit) * group(s.fit) + (rest ? group(rest) : 0.0f);
+      if (S > 1) t += 4.0f + (float)S * M * N * 8.0f / 7.4e6f;
+      if (!best.wm || t < least) {
+        best = Plan16{s.wm, s.wn, s.ns, S};
+        least = t;
+      }
+    }
+  }
+  return best;
+}
+
 size_t linear_part_floats(bool bf16_io, Prod p, int M, int N, int K) {
   const int a = p == Prod::Gw ? N : M, b = p == Prod::Fwd ? N : K, k = p == Prod::Fwd ? K : p == Prod::Gx ? N : M;
   if (!a || !k) return 0;
-  const int S = bf16_io ? plan16(a, b, k).S : slices32(a, b, k);
+  int S = bf16_io ? plan16(a, b, k).S : slices32(a, b, k);
+  if (bf16_io && p == Prod::Gw && !gw_unpacked_floats(M, K)) S = std::max(S, slices32(a, b, k));
   return (S > 1 ? (size_t)S * a * b : 0) + (bf16_io && p == Prod::Gw ? gw_unpacked_floats(M, K) : 0);
 }
 
 hipError_t launch_linear_fwd(bool bf16_io, const void* x, const void* w, int M, int N, int K, const Epi& ep,
                              float* part, hipStream_t st) {
-  if (bf16_io) return run16(false, false, x, K, M, w, K, N, K, ep, part, st);
+  if (bf16_io) return run16(launch_tile16_fwd, x, K, M, w, K, N, K, ep, part, st);
   const Operand a{x, nullptr, K, M}, b{w, nullptr, K, N};
   return run32<float, SRC_ROWK, SRC_ROWK>(a, b, K, ep, part, st);
 }
 
 hipError_t launch_linear_gx(bool bf16_io, const void* gz, const void* w, int M, int N, int K, void* gx, float* part,
                             hipStream_t st) {
-  if (bf16_io) return run16(false, true, gz, N, M, w, K, K, N, plain_out(gx), part, st);
+  if (bf16_io) return run16(launch_tile16_gx, gz, N, M, w, K, K, N, plain_out(gx), part, st);
   const Operand a{gz, nullptr, N, M}, b{w, nullptr, K, K};
   return run32<float, SRC_ROWK, SRC_KMAJ>(a, b, N, plain_out(gx), part, st);
 }
@@ -253,16 +300,17 @@ hipError_t launch_linear_gx(bool bf16_io, const void* gz, const void* w, int M, 
 hipError_t launch_linear_gw(bool bf16_io, const void* gz, const void* x, Ckpt xc, int M, int N, int K, void* gw,
                             float* part, hipStream_t st) {
   const Epi ep = plain_out(gw);
-  if (bf16_io && M > 0) {  // (no rows: zeros, from the kernel below)
+  if (bf16_io && M > 0 && (!xc.q || gw_unpacked_floats(M, K))) {  // (no rows: zeros, from the kernel below)
     if (xc.q) {
       const hipError_t e = launch_ckpt_unpack(true, xc, M, K, part, st);
       if (e != hipSuccess) return e;
       x = part;
       part += gw_unpacked_floats(M, K);
     }
-    return run16(true, true, gz, N, N, x, K, K, M, ep, part, st);
+    return run16(launch_tile16_gw, gz, N, N, x, K, K, M, ep, part, st);
   }
   const Operand a{gz, nullptr, N, N}, b{xc.q ? (const void*)xc.q : x, xc.scale, K, K};
+  if (bf16_io && xc.q) return run32<bf16, SRC_KMAJ, SRC_KMAJ_Q8>(a, b, M, ep, part, st);
   if (bf16_io) return run32<bf16, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st);
   if (xc.q) return run32<float, SRC_KMAJ, SRC_KMAJ_Q8>(a, b, M, ep, part, st);
   return run32<float, SRC_KMAJ, SRC_KMAJ>(a, b, M, ep, part, st);

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "common.hpp"
 
 namespace instant {
@@ -20,6 +22,15 @@ struct Ckpt {
   int8_t* q;
   uint8_t* scale;
 };
+
+// f(0) .. f(N - 1) with constant arguments: register arrays are indexed by constants whatever
+// the size of the body
+template <int... I, class F> __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void each(F&& f) {
+  each(std::make_integer_sequence<int, N>{}, f);
+}
 
 // ---- the checkpoint format on the device
 
@@ -42,15 +53,14 @@ __device__ __forceinline__ float ck_inv_scale(unsigned byte) { return __builtin_
 
 // Eight values to int8 (nearest, ties to even): packed low to high.
 __device__ __forceinline__ uint2 ck_quant8(const float v[8], unsigned byte) {
-  if (byte == 255u) return uint2{0u, 0u};
-  const float inv = ck_inv_scale(byte);
+  const float inv = ck_inv_scale(byte == 255u ? 254u : byte);
   unsigned r[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     unsigned p = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) p |= ((unsigned)(int)__builtin_rintf(v[4 * h + j] * inv) & 0xffu) << (8 * j);
-    r[h] = p;
+    r[h] = byte == 255u ? 0u : p;
   }
   return uint2{r[0], r[1]};
 }
@@ -149,18 +159,19 @@ template <int ACT, bool FAST> __device__ __forceinline__ float act_slope(float z
   return 1.0f;
 }
 
-template <bool FAST> __device__ __forceinline__ void act_fwd8(int act, float v[8]) {
-#define INSTANT_ACT8(A)                                       \
-  case A:                                                     \
-    _Pragma("unroll") for (int j = 0; j < 8; ++j) v[j] = act_fwd<A, FAST>(v[j]); \
+template <bool FAST, int NB> __device__ __forceinline__ void act_fwd_all(int act, float (&v)[NB][8]) {
+#define INSTANT_ACT(A)                                                                     \
+  case A:                                                                                  \
+    _Pragma("unroll") for (int k = 0; k < NB; ++k)                                         \
+        _Pragma("unroll") for (int j = 0; j < 8; ++j) v[k][j] = act_fwd<A, FAST>(v[k][j]); \
     break;
   switch (act) {
-    INSTANT_ACT8(ACT_RELU)
-    INSTANT_ACT8(ACT_GELU)
-    INSTANT_ACT8(ACT_GELU_TANH)
-    INSTANT_ACT8(ACT_SILU)
+    INSTANT_ACT(ACT_RELU)
+    INSTANT_ACT(ACT_GELU)
+    INSTANT_ACT(ACT_GELU_TANH)
+    INSTANT_ACT(ACT_SILU)
   }
-#undef INSTANT_ACT8
+#undef INSTANT_ACT
 }
 
 // ---- vectors of 8 elements
@@ -181,36 +192,63 @@ struct Epi {
   int act;
 };
 
-// Eight consecutive columns n .. n+7 (n % 8 == 0) of row m. The four lanes that differ in
-// lane-id bits X1, X2 hold the 32-column group of n and must all call; `in` is false where
-// (m, n) lies outside the output.
-template <class T, int X1, int X2>
-__device__ __forceinline__ void epilogue8(const Epi& ep, float v[8], int m, int n, int N, bool in) {
+template <class T> __device__ __forceinline__ void load_bias(const Epi& ep, int n, int N, float b[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+  if (ep.bias && n < N) load8((const T*)ep.bias + n, b);
+}
+
+// The eight consecutive columns n .. n+7 (n % 8 == 0) of rows m, m + step, ... (NB of them, each
+// `in` the output or not): their bias, their residuals r (anything without one) and their sums v,
+// which are used up. The four lanes that differ in lane-id bits X1, X2 hold the 32-column group
+// of n and must all call.
+template <class T, int NB, int X1, int X2>
+__device__ __forceinline__ void epilogue(const Epi& ep, const float bias[8], const typename MM<T>::vec8 (&r)[NB],
+                                         float (&v)[NB][8], int m, int step, int n, int N, const bool (&in)[NB]) {
   constexpr bool FAST = sizeof(T) == 2;
-  const size_t at = (size_t)m * N + n;
-  if (in && ep.bias) {
-    float b[8];
-    load8((const T*)ep.bias + n, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] += bias[j];
   if (ep.zc.q) {
-    const unsigned byte = ck_scale_byte(ck_group_amax<X1, X2>(v, in));
-    if (in) {
-      *reinterpret_cast<uint2*>(ep.zc.q + at) = ck_quant8(v, byte);
-      if (n % CK_GROUP == 0) ep.zc.scale[(size_t)m * ck_groups(N) + n / CK_GROUP] = (uint8_t)byte;
-    }
-  }
-  if (!in) return;
-  if (ep.z) store_row<T, 8>((T*)ep.z + at, v);
-  act_fwd8<FAST>(ep.act, v);
-  if (ep.res) {
-    float r[8];
-    load8((const T*)ep.res + at, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
+    for (int k = 0; k < NB; ++k) {
+      const unsigned byte = ck_scale_byte(ck_group_amax<X1, X2>(v[k], in[k]));
+      if (in[k]) {
+        const size_t row = m + k * step;
+        *reinterpret_cast<uint2*>(ep.zc.q + row * N + n) = ck_quant8(v[k], byte);
+        if (n % CK_GROUP == 0) ep.zc.scale[row * ck_groups(N) + n / CK_GROUP] = (uint8_t)byte;
+      }
+    }
+  } else if (ep.z) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+      if (in[k]) store_row<T, 8>((T*)ep.z + (size_t)(m + k * step) * N + n, v[k]);
   }
-  store_row<T, 8>((T*)ep.y + at, v);
+  act_fwd_all<FAST, NB>(ep.act, v);
+  if (ep.res) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] += (float)r[k][j];
+  }
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+    if (in[k]) store_row<T, 8>((T*)ep.y + (size_t)(m + k * step) * N + n, v[k]);
+}
+
+// One row of it.
+template <class T, int X1, int X2>
+__device__ __forceinline__ void epilogue8(const Epi& ep, float (&v)[8], int m, int n, int N, bool in) {
+  float bias[8], w[1][8];
+  typename MM<T>::vec8 r[1];
+  r[0] = zero_vec8<T>();
+  load_bias<T>(ep, n, N, bias);
+  if (in && ep.res) r[0] = *reinterpret_cast<const typename MM<T>::vec8*>((const T*)ep.res + (size_t)m * N + n);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[0][j] = v[j];
+  const bool ok[1] = {in};
+  epilogue<T, 1, X1, X2>(ep, bias, r, w, m, 0, n, N, ok);
 }
 
 // ---- host launchers (each returns the launch status; pointers are device pointers)

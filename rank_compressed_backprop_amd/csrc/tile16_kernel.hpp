@@ -5,22 +5,21 @@
 // every operand byte read from LDS then feeds 128 products, and the LDS reads of a stage (64 k)
 // take half the matrix cores' time (a wave tile of 64 x 64 would take all of it).
 //
-// A stage goes from memory straight to LDS (16 bytes a lane); two stages are held. A wave runs
+// A stage goes from memory straight to LDS (16 bytes a lane); NS stages are held. A wave runs
 // two half stages of 32 k by turns from two sets of operand registers:
 //   multiply half 0 of stage s   while half 1 of s is read from LDS
 //   wait for stage s + 1, barrier: every wave has read all of s
-//   multiply half 1 of stage s   while half 0 of s + 1 is read and stage s + 2 is requested
+//   multiply half 1 of stage s   while half 0 of s + 1 is read and stage s + NS is requested
 //                                into the slot of s
-// so the matrix cores always have operands in registers, and a request has the time of a whole
-// stage to arrive. The reads and requests are dealt out between the products by hand.
+// so the matrix cores always have operands in registers, and a request has the time of NS - 1
+// stages to arrive. The reads and requests are dealt out between the products by hand.
 //
 // Rows (columns) of a tile that lie outside the operand are read from its last row (column
 // chunk) instead: they only reach outputs that are not stored. Behind the contraction's end the
 // last k is read again, and its place in LDS cleared by the lane that read it. Past the last
 // stage the last one is requested again, so the loop has no branch around its products (with
 // one, the compiler copies the 256 accumulators).
-#include <algorithm>
-#include <utility>
+#pragma once
 
 #include "dma.hpp"
 #include "lds_tiles.hpp"
@@ -32,15 +31,6 @@ namespace instant {
 namespace {
 
 constexpr int K16 = 64;  // k per stage
-
-// f(0) .. f(N - 1) with constant arguments: register arrays are indexed by constants whatever
-// the size of the body
-template <int... I, class F> __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F> __device__ __forceinline__ void each(F&& f) {
-  each(std::make_integer_sequence<int, N>{}, f);
-}
 
 // 16 bytes per lane from base + off (base uniform) straight into LDS at lds_wave + 16 * lane.
 __device__ __forceinline__ void lds_dma16_at(const void* base, unsigned off, void* lds_wave) {
@@ -126,19 +116,21 @@ struct Side {
         *reinterpret_cast<f32x4*>(lds + 1024 * (j * 4 + wave) + 16 * lane) = zero4();
     });
   }
-  // the MFMA operand of 16-row tile `t` (first row 16 t of the tile) and k half h
-  __device__ static __forceinline__ bf16x8 frag(const unsigned char* lds, int t, int h, int lane) {
+  // LDS reads that make one MFMA operand, and read `part` of the operand of 16-row tile `t` (first
+  // row 16 t of the tile), k half h
+  static constexpr int PARTS = KMAJ ? 2 : 1;
+  __device__ static __forceinline__ void read(bf16x8& f, int part, const unsigned char* lds, int t, int h, int lane) {
     if constexpr (!KMAJ) {
       const int r = 16 * t + (lane & 15);
-      return *reinterpret_cast<const bf16x8*>(lds + r * 128 + 16 * ((4 * h + (lane >> 4)) ^ (r & 7)));
+      f = *reinterpret_cast<const bf16x8*>(lds + r * 128 + 16 * ((4 * h + (lane >> 4)) ^ (r & 7)));
     } else {
       const int q = lane >> 4, s = lane & 15, a = s & 3;
       const int col0 = PAIR ? 32 * (t >> 1) : 16 * t;
       const int col = PAIR ? col0 + 8 * a + 4 * ((t & 1) ^ (a & 1)) : col0 + 4 * a;
       const int r0 = 32 * h + 8 * q + (s >> 2);  // and row r0 + 4, which has the same swizzle
-      const unsigned char* p = lds + r0 * (2 * W) + 16 * ((col >> 3) ^ swz(r0)) + (col & 7) * 2;
-      const bf16x4 lo = tr_read(p), hi = tr_read(p + 8 * W);
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const bf16x4 v = tr_read(lds + (r0 + 4 * part) * (2 * W) + 16 * ((col >> 3) ^ swz(r0)) + (col & 7) * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[4 * part + j] = v[j];
     }
   }
 };
@@ -147,7 +139,7 @@ struct Side {
 
 // C(m, n) = sum_k A(m, k) B(n, k) over k slice blockIdx.z. WM x WN: 16-row tiles of a wave
 // (WN even); the waves form a 2 x 2 grid. Grid (tiles, 1, S).
-template <bool AKM, bool BKM, int WM, int WN, bool PART>
+template <bool AKM, bool BKM, int WM, int WN, int NS, bool PART>
 __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__ A, int lda, int M,
                                                         const bf16* __restrict__ B, int ldb, int N, int K, Epi ep,
                                                         float* __restrict__ part) {
@@ -155,7 +147,11 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   typedef Side<AKM, false, BM> SA;
   typedef Side<BKM, true, BN> SB;
   constexpr int STAGE = SA::BYTES + SB::BYTES;
-  __shared__ __attribute__((aligned(1024))) unsigned char ring[2][STAGE];
+  // rows a wave turns at a time at the end, and the floats of one (4 more than its columns, for
+  // the banks)
+  constexpr int ROWS = WM == 8 ? 64 : 32, LDO = 16 * WN + 4;
+  constexpr int TURN = 4 * ROWS * LDO * 4;
+  __shared__ __attribute__((aligned(1024))) unsigned char ring[NS * STAGE > TURN ? NS * STAGE : TURN];
   const int lane = threadIdx.x & (WAVE - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int mt = (M + BM - 1) / BM, nt = (N + BN - 1) / BN;
@@ -163,7 +159,7 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   tile_of(xcd_unit(blockIdx.x, mt * nt), mt, nt, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   const int nst = (K + K16 - 1) / K16, S = gridDim.z, z = blockIdx.z;
-  const int s0 = (int)((long)nst * z / S), nq = (int)((long)nst * (z + 1) / S) - s0;
+  const int s0 = (int)((unsigned)nst * z / S), nq = (int)((unsigned)nst * (z + 1) / S) - s0;  // (nst <= 2^20)
   const int wm = wave >> 1, wn = wave & 1;
 
   SA sa;
@@ -199,29 +195,31 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
 #pragma unroll
     for (int j = 0; j < WN; ++j) acc[i][j] = zero4();
   bf16x8 fa[2][WM], fb[2][WN];
-  constexpr int NREAD = WM + WN, NMMA = WM * WN;
-  auto read = [&](auto r, auto set, const unsigned char* st) {  // operand r of half `set`
-    if constexpr (r < WN) fb[set][r] = SB::frag(st + SA::BYTES, WN * wn + r, set, lane);
-    else fa[set][r - WN] = SA::frag(st, WM * wm + r - WN, set, lane);
+  constexpr int NMMA = WM * WN, NRB = WN * SB::PARTS, NREAD = NRB + WM * SA::PARTS;
+  auto read = [&](auto r, auto set, const unsigned char* st) {  // LDS read r of half `set`
+    if constexpr (r < NRB) {
+      constexpr int j = r / SB::PARTS;
+      SB::read(fb[set][j], r % SB::PARTS, st + SA::BYTES, WN * wn + j, set, lane);
+    } else {
+      constexpr int i = (r - NRB) / SA::PARTS;
+      SA::read(fa[set][i], (r - NRB) % SA::PARTS, st, WM * wm + i, set, lane);
+    }
   };
   // The products of one half, with the reads of operand set `to` from st and (DMA) the requests
-  // into slot dealt out over the first three quarters of them.
+  // into slot dealt out evenly between them: a request holds the wave for the time of one
+  // product, so two events in one place would leave the matrix cores idle.
   auto half = [&](auto set, auto to, auto dma, const unsigned char* st, unsigned char* slot) {
+    constexpr int ND = decltype(dma)::value ? NDMA : 0, NE = NREAD + ND;
     each<NMMA>([&](auto t) {
       acc[t / WN][t % WN] = MM<bf16>::mma(fb[set][t % WN], fa[set][t / WN], acc[t / WN][t % WN]);
-      each<NREAD>([&](auto r) {
-        if constexpr (r * (NMMA * 3 / 4) / NREAD == t) {
-          read(r, to, st);
+      each<NE>([&](auto e) {
+        if constexpr (e * NMMA / NE == t) {
+          constexpr int d = e * ND / NE;  // requests before event e
+          if constexpr ((e + 1) * ND / NE > d) request(d, slot);
+          else read(std::integral_constant<int, e - d>{}, to, st);
           __builtin_amdgcn_sched_barrier(0);
         }
       });
-      if constexpr (decltype(dma)::value)
-        each<NDMA>([&](auto j) {
-          if constexpr (j * (NMMA * 3 / 4) / NDMA == t) {
-            request(j, slot);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        });
     });
   };
   // stage s has arrived for this wave: clear what lies behind the contraction's end
@@ -236,21 +234,23 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   constexpr std::integral_constant<int, 1> h1{};
 
 #pragma unroll 1
-  for (int q = 0; q < 2; ++q) {
-    each<NDMA>([&](auto j) { request(j, ring[q]); });
+  for (int q = 0; q < NS; ++q) {
+    each<NDMA>([&](auto j) { request(j, ring + q * STAGE); });
     advance();
   }
-  wait_vmcnt<NDMA>();
-  arrived(0, ring[0]);
+  wait_vmcnt<(NS - 1) * NDMA>();
+  arrived(0, ring);
   bare_barrier();
-  each<NREAD>([&](auto r) { read(r, h0, ring[0]); });
+  each<NREAD>([&](auto r) { read(r, h0, ring); });
 
+  int slot = 0;
 #pragma unroll 1
   for (int s = 0; s < nq; ++s) {
-    unsigned char* cur = ring[s & 1];
-    unsigned char* nxt = ring[(s & 1) ^ 1];
+    unsigned char* cur = ring + slot * STAGE;
+    slot = slot + 1 == NS ? 0 : slot + 1;
+    unsigned char* nxt = ring + slot * STAGE;
     half(h0, h1, std::false_type{}, cur, nullptr);
-    wait_vmcnt<0>();  // stage s + 1 is here, and this wave's reads of s are done
+    wait_vmcnt<(NS - 2) * NDMA>();  // stage s + 1 is here, and this wave's reads of s are done
     arrived(s + 1, nxt);
     bare_barrier();
     // (after the last stage what is read and requested goes unused)
@@ -262,80 +262,95 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   // to and fro inside the loop for the epilogue's sake: 1.6 times the loop's time)
   each<WM>([&](auto i) { each<WN>([&](auto j) { keep_in_agprs(acc[i][j]); }); });
 
+  // Out through LDS: each wave turns ROWS rows of its tile at a time, so that the epilogue is one
+  // small loop over 8 columns a lane with whole rows stored by neighbouring lanes. (Unrolled over
+  // the accumulators it was 100 KB of code, fetched cold by every block: 15 us of a block's time.)
+  bare_barrier();  // every wave is done with the ring
+  float* mine = reinterpret_cast<float*>(ring) + wave * ROWS * LDO;
   const int q4 = lane >> 4, l16 = lane & 15;
-  each<WM>([&](auto i) {
-    const int m = m0 + 16 * (WM * wm + i) + l16;
-    each<WN / 2>([&](auto p) {
-      const int n = n0 + 16 * WN * wn + 32 * p + 8 * q4;
-      const bool in = m < M && n < N;
-      // the k-major layout's halves alternate: this lane's first four columns are in tile
-      // q4 % 2 of the pair (lds_tiles.hpp)
-      const bool sw = BKM && (q4 & 1);
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = acc[i][2 * p][j], b = acc[i][2 * p + 1][j];
-        v[j] = sw ? b : a;
-        v[4 + j] = sw ? a : b;
-      }
-      if constexpr (PART) {
-        if (in) store_row<float, 8>(part + ((size_t)z * M + m) * N + n, v);
-      } else {
-        epilogue8<bf16, 16, 32>(ep, v, m, n, N, in);
-      }
+  // the k-major layout's halves alternate: this lane's first four columns of a pair are in tile
+  // q4 % 2 of it (lds_tiles.hpp)
+  const int lo = BKM && (q4 & 1) ? 4 : 0;
+  // lane -> row of a batch's RPI rows and 8 of its columns; four neighbouring lanes hold a group
+  // of 32 columns. NB batches at a time, so that their loads, exponentials and stores overlap.
+  constexpr int UPR = 2 * WN, RPI = WAVE / UPR, NB = 4;
+  const int row = lane / UPR, col = lane % UPR, n = n0 + 16 * WN * wn + 8 * col;
+  float bias[8];
+  if constexpr (!PART) load_bias<bf16>(ep, n, N, bias);
+  auto fetch_res = [&](bf16x8 (&r)[NB], int mr) {
+    if (ep.res)
+      each<NB>([&](auto k) {
+        const int m = mr + k * RPI;
+        if (m < M && n < N) r[k] = *reinterpret_cast<const bf16x8*>((const bf16*)ep.res + (size_t)m * N + n);
+      });
+  };
+  each<WM * 16 / ROWS>([&](auto c) {
+    each<ROWS / 16>([&](auto i) {
+      each<WN>([&](auto j) {
+        *reinterpret_cast<f32x4*>(mine + (16 * i + l16) * LDO + 32 * (j / 2) + 8 * q4 + ((j & 1) ? 4 - lo : lo)) =
+            acc[c * (ROWS / 16) + i][j];
+      });
     });
+    const int mb = m0 + 16 * WM * wm + ROWS * c + row;
+    bf16x8 r[NB];
+    if constexpr (!PART) fetch_res(r, mb);
+#pragma unroll 1
+    for (int it = 0; it < ROWS; it += RPI * NB) {
+      float v[NB][8];
+      bool in[NB];
+      each<NB>([&](auto k) {
+        const int dr = it + k * RPI;
+        in[k] = row < RPI && row + dr < ROWS && mb + dr < M && n < N;
+        load8(mine + min(row + dr, ROWS - 1) * LDO + 8 * col, v[k]);
+      });
+      if constexpr (PART) {
+        each<NB>([&](auto k) {
+          if (in[k]) store_row<float, 8>(part + ((size_t)z * M + mb + it + k * RPI) * N + n, v[k]);
+        });
+      } else {
+        bf16x8 rc[NB];
+        each<NB>([&](auto k) { rc[k] = r[k]; });
+        if (it + RPI * NB < ROWS) fetch_res(r, mb + it + RPI * NB);  // before this batch's stores
+        epilogue<bf16, NB, 1, 2>(ep, bias, rc, v, mb + it, RPI, n, N, in);
+      }
+    }
   });
 }
 
 namespace {
 
-template <bool AKM, bool BKM, int WM, int WN>
+template <bool AKM, bool BKM, int WM, int WN, int NS>
 hipError_t go16(const bf16* A, int lda, int M, const bf16* B, int ldb, int N, int K, const Epi& ep, int S, float* part,
                 hipStream_t st) {
   const unsigned tiles = (unsigned)((M + 32 * WM - 1) / (32 * WM)) * ((N + 32 * WN - 1) / (32 * WN));
   if (S > 1)
-    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, true>), dim3(tiles, 1, S), dim3(256), 0, st, A, lda, M, B, ldb,
+    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, NS, true>), dim3(tiles, 1, S), dim3(256), 0, st, A, lda, M, B, ldb,
                        N, K, ep, part);
   else
-    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, false>), dim3(tiles), dim3(256), 0, st, A, lda, M, B, ldb, N, K,
+    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, NS, false>), dim3(tiles), dim3(256), 0, st, A, lda, M, B, ldb, N, K,
                        ep, part);
   return hipGetLastError();
 }
 
-}  // namespace
-
-Plan16 plan16(int M, int N, int K) {
-  // rounds of blocks over the 256 compute units times a block's time, which goes with its area
-  // (and a floor for its operands' stages)
-  static const int shapes[][2] = {{8, 8}, {8, 6}, {8, 4}, {4, 4}};
-  Plan16 best{0, 0, 1};
-  double least = 0;
-  for (const auto& s : shapes) {
-    const int bm = 32 * s[0], bn = 32 * s[1];
-    const long tiles = (long)((M + bm - 1) / bm) * ((N + bn - 1) / bn);
-    const int per_cu = s[0] == 4 ? 2 : 1;  // blocks that share a compute unit
-    const double rounds = (double)((tiles + 256 * per_cu - 1) / (256 * per_cu)) * per_cu;
-    const double cost = rounds * (bm * bn + 24.0 * (bm + bn));
-    if (!best.wm || cost < least) {
-      best = Plan16{s[0], s[1], 1};
-      least = cost;
-    }
-  }
-  const long tiles = (long)((M + 32 * best.wm - 1) / (32 * best.wm)) * ((N + 32 * best.wn - 1) / (32 * best.wn));
-  const int nst = (K + K16 - 1) / K16;
-  while (tiles * best.S * 2 <= 512 && best.S < 16 && nst / (2 * best.S) >= 4) best.S *= 2;
-  return best;
-}
-
-hipError_t launch_tile16(bool akm, bool bkm, const void* A, int lda, int M, const void* B, int ldb, int N, int K,
-                         const Epi& ep, float* part, hipStream_t st) {
+// The launch for one pair of layouts (each layout is compiled in a file of its own).
+template <bool AKM, bool BKM>
+hipError_t launch16(const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep, float* part,
+                    hipStream_t st) {
   const Plan16 p = plan16(M, N, K);
-#define GO(AK, BK, WM, WN) go16<AK, BK, WM, WN>((const bf16*)A, lda, M, (const bf16*)B, ldb, N, K, ep, p.S, part, st)
-#define GO_SHAPE(AK, BK)                                                                                        \
-  (p.wm == 4 ? GO(AK, BK, 4, 4) : p.wn == 8 ? GO(AK, BK, 8, 8) : p.wn == 6 ? GO(AK, BK, 8, 6) : GO(AK, BK, 8, 4))
-  return akm ? GO_SHAPE(true, true) : bkm ? GO_SHAPE(false, true) : GO_SHAPE(false, false);
-#undef GO_SHAPE
+#define GO(WM, WN, NS)                  \
+  if (p.wm == WM && p.wn == WN && p.ns == NS) \
+    return go16<AKM, BKM, WM, WN, NS>((const bf16*)A, lda, M, (const bf16*)B, ldb, N, K, ep, p.S, part, st)
+  GO(8, 8, 2);
+  GO(8, 6, 2);
+  GO(4, 4, 2);
+  GO(4, 4, 4);
+  GO(2, 4, 3);
+  GO(2, 4, 2);
+  GO(2, 2, 2);
+  GO(2, 2, 4);
 #undef GO
+  return hipErrorInvalidValue;
 }
 
+}  // namespace
 }  // namespace instant
