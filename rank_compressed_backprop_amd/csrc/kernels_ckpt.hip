@@ -84,13 +84,15 @@ hipError_t launch_ckpt_unpack(bool bf16_io, Ckpt c, int M, int C, void* x, hipSt
 // ---- gz = gy * act'(z), gb = sum_m gz
 //
 // A block takes 256 columns (32 threads of 8) of a strip of rows (8 threads deep); the strip's
-// column sums are reduced over the 8 in LDS and left as part[strip][N], which act_gb_kernel adds
-// in strip order. gz is summed before its rounding.
+// column sums are reduced over the 8 in LDS and left as part[strip][N], which the column sum adds
+// in a fixed order. Up to 128 rows there is one strip, and its sums are gb (a second launch costs
+// the host 4 us, a thread's 16 rows less). gz is summed before its rounding.
 
 namespace {
 constexpr int AB_COLS = 256, AB_DEEP = 8;
 
 int act_strips(int M, int N) {
+  if (M <= 128) return 1;
   const int cb = (N + AB_COLS - 1) / AB_COLS;
   int strips = std::min(256, std::max(1, 2048 / cb));
   return std::max(1, std::min(strips, (M + AB_DEEP - 1) / AB_DEEP));
@@ -99,7 +101,7 @@ int act_strips(int M, int N) {
 
 template <class T, int ACT, bool Q8>
 __global__ __launch_bounds__(256) void act_bwd_kernel(const T* gy, const T* z, Ckpt zc, int M, int N, T* gz,
-                                                      float* __restrict__ part) {
+                                                      T* __restrict__ gb, float* __restrict__ part) {
   constexpr bool FAST = sizeof(T) == 2;
   __shared__ float sums[AB_DEEP][AB_COLS + 4];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const T* gy, const T* z, C
       for (int j = 0; j < 8; ++j) sum[j] += g[j];
     }
   }
-  if (!part) return;
+  if (!gb) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[ry][8 * cx + j] = sum[j];
   __syncthreads();
@@ -139,7 +141,8 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const T* gy, const T* z, C
     float v = 0.0f;
 #pragma unroll
     for (int r = 0; r < AB_DEEP; ++r) v += sums[r][threadIdx.x];
-    part[(size_t)s * N + c] = v;
+    if (strips == 1) gb[c] = from_f32<T>(v);
+    else part[(size_t)s * N + c] = v;
   }
 }
 
@@ -176,17 +179,17 @@ hipError_t launch_column_sum(bool bf16_io, const float* part, int S, int N, void
   return hipGetLastError();
 }
 
-size_t act_bwd_part_floats(int M, int N) { return M ? (size_t)act_strips(M, N) * N : 0; }
+size_t act_bwd_part_floats(int M, int N) { const int S = M ? act_strips(M, N) : 0;
+  return S > 1 ? (size_t)S * N : 0; }
 
 hipError_t launch_act_bwd(bool bf16_io, const void* gy, const void* z, Ckpt zc, int M, int N, int act, void* gz,
                           void* gb, float* part, hipStream_t st) {
   const int S = M ? act_strips(M, N) : 0;
   if (M) {
     const dim3 grid((N + AB_COLS - 1) / AB_COLS, S);
-    if (!gb) part = nullptr;
 #define ACTB(T, A, Q)                                                                                             \
   hipLaunchKernelGGL((act_bwd_kernel<T, A, Q>), grid, dim3(256), 0, st, (const T*)gy, (const T*)z, zc, M, N, (T*)gz, \
-                     part)
+                     (T*)gb, part)
 #define ACTB_Q(T, A)      \
   case A:                 \
     if (zc.q) ACTB(T, A, true); \
@@ -208,7 +211,7 @@ hipError_t launch_act_bwd(bool bf16_io, const void* gy, const void* z, Ckpt zc, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return gb ? launch_column_sum(bf16_io, part, S, N, gb, st) : hipSuccess;
+  return gb && S != 1 ? launch_column_sum(bf16_io, part, S, N, gb, st) : hipSuccess;
 }
 
 }  // namespace instant

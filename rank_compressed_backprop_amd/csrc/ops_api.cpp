@@ -85,6 +85,21 @@ INSTANT_API size_t instant_linear_workspace_bytes(int32_t M, int32_t N, int32_t 
                             4 * act_bwd_part_floats(M, N)}));
 }
 
+INSTANT_API size_t instant_linear_fwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {
+  if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
+  return linear_fwd_bytes(dtype == INSTANT_BF16, M, N, K);
+}
+
+INSTANT_API size_t instant_linear_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {
+  if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
+  return linear_bwd_bytes(dtype == INSTANT_BF16, M, N, K);
+}
+
+INSTANT_API size_t instant_act_bwd_workspace_bytes(int32_t M, int32_t N, int32_t dtype) {
+  if (sizes(M, {N}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
+  return 4 * act_bwd_part_floats(M, N);
+}
+
 INSTANT_API instant_status instant_linear_fwd(const void* x, const void* w, const void* bias, const void* res,
                                               int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t act, void* y,
                                               void* z, void* zq, void* zscale, void* workspace,

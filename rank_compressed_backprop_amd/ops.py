@@ -13,6 +13,7 @@ build the layers.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -28,6 +29,9 @@ _sig = {
     "instant_ckpt_pack": (_st, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "instant_ckpt_unpack": (_st, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "instant_linear_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_linear_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_act_bwd_workspace_bytes": (_sz, [_i, _i, _i]),
     "instant_linear_fwd": (_st, [_vp] * 4 + [_i] * 5 + [_vp] * 5 + [_sz, _vp]),
     "instant_act_bwd": (_st, [_vp] * 4 + [_i] * 4 + [_vp] * 3 + [_sz, _vp]),
     "instant_linear_bwd": (_st, [_vp] * 5 + [_i] * 4 + [_vp] * 3 + [_sz, _vp]),
@@ -55,6 +59,18 @@ def instant_ckpt_unpack(q, scale, M, C, dtype, x, stream=None) -> int:
 
 def instant_linear_workspace_bytes(M, N, K, dtype) -> int:
     return int(_lib.instant_linear_workspace_bytes(M, N, K, dtype))
+
+
+def instant_linear_fwd_workspace_bytes(M, N, K, dtype) -> int:
+    return int(_lib.instant_linear_fwd_workspace_bytes(M, N, K, dtype))
+
+
+def instant_linear_bwd_workspace_bytes(M, N, K, dtype) -> int:
+    return int(_lib.instant_linear_bwd_workspace_bytes(M, N, K, dtype))
+
+
+def instant_act_bwd_workspace_bytes(M, N, dtype) -> int:
+    return int(_lib.instant_act_bwd_workspace_bytes(M, N, dtype))
 
 
 def instant_linear_fwd(x, w, bias, res, M, N, K, dtype, act, y, z, zq, zscale, workspace, workspace_bytes,
@@ -135,10 +151,29 @@ def _like(t, shape, dtype, device, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(n, device):
+# Sizes depend on the shapes alone.
+_fwd_bytes = functools.lru_cache(4096)(instant_linear_fwd_workspace_bytes)
+_bwd_bytes = functools.lru_cache(4096)(instant_linear_bwd_workspace_bytes)
+_act_bytes = functools.lru_cache(4096)(instant_act_bwd_workspace_bytes)
+_norm_bytes = functools.lru_cache(4096)(instant_rmsnorm_workspace_bytes)
+
+
+def _workspace(n, like):
+    """n bytes of workspace (None if none are needed) and their address. The caller keeps the
+    tensor until its launches are enqueued; the allocator orders its reuse after them."""
     if n == 0:
-        raise ValueError("sizes outside what the operator takes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        return None, None
+    ws = like.new_empty(n, dtype=torch.uint8)
+    return ws, ws.data_ptr()
+
+
+# The current stream of the current device, on which every input lies.
+def _current(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def _act(name):
@@ -161,39 +196,40 @@ class Checkpoint8(NamedTuple):
         return self.q.shape
 
 
-def _groups(C):
-    return -(-C // CKPT_GROUP)
-
-
-def _empty_ckpt(shape, device):
-    return Checkpoint8(torch.empty(shape, dtype=torch.int8, device=device),
-                       torch.empty((*shape[:-1], _groups(shape[-1])), dtype=torch.uint8, device=device))
+def _empty_ckpt(shape, like):
+    return Checkpoint8(like.new_empty(shape, dtype=torch.int8),
+                       like.new_empty((*shape[:-1], -(-shape[-1] // CKPT_GROUP)), dtype=torch.uint8))
 
 
 def _ckpt(c, shape, device, name):
-    _like(c.q, shape, torch.int8, device, f"{name}.q")
-    _like(c.scale, torch.Size((*shape[:-1], _groups(shape[-1]))), torch.uint8, device, f"{name}.scale")
+    _like(c.q, shape, torch.int8, device, name + ".q")
+    _like(c.scale, (*shape[:-1], -(-shape[-1] // CKPT_GROUP)), torch.uint8, device, name + ".scale")
 
 
 def checkpoint_pack(x) -> Checkpoint8:
     """x [..., C] in 8 bits."""
     M, C, dt = _matrix(x, "x")
-    c = _empty_ckpt(x.shape, x.device)
-    _ok(instant_ckpt_pack(x, M, C, dt, c.q, c.scale), "instant_ckpt_pack")
+    c = _empty_ckpt(x.shape, x)
+    _ok(_lib.instant_ckpt_pack(x.data_ptr(), M, C, dt, c.q.data_ptr(), c.scale.data_ptr(), _current(x.get_device())),
+        "instant_ckpt_pack")
     return c
 
 
 def checkpoint_unpack(c: Checkpoint8, dtype=torch.bfloat16) -> torch.Tensor:
     """The values of a checkpoint (exact in both types)."""
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    if c.q.dim() < 1 or c.q.shape[-1] < 8 or c.q.shape[-1] % 8:
-        raise ValueError(f"a checkpoint's last dimension is a positive multiple of 8, got {tuple(c.q.shape)}")
-    _on_device(c.q, "q")
-    _ckpt(c, c.q.shape, c.q.get_device(), "checkpoint")
-    C = c.q.shape[-1]
-    x = torch.empty(c.q.shape, dtype=dtype, device=c.q.device)
-    _ok(instant_ckpt_unpack(c.q, c.scale, c.q.numel() // C, C, _DTYPES[dtype], x), "instant_ckpt_unpack")
+    q, shape = c.q, c.q.shape
+    if q.dim() < 1 or shape[-1] < 8 or shape[-1] % 8:
+        raise ValueError(f"a checkpoint's last dimension is a positive multiple of 8, got {tuple(shape)}")
+    _on_device(q, "q")
+    dev = q.get_device()
+    _ckpt(c, shape, dev, "checkpoint")
+    C = shape[-1]
+    x = torch.empty_like(q, dtype=dtype)
+    _ok(_lib.instant_ckpt_unpack(q.data_ptr(), c.scale.data_ptr(), q.numel() // C, C, code, x.data_ptr(),
+                                 _current(dev)), "instant_ckpt_unpack")
     return x
 
 
@@ -211,20 +247,27 @@ def linear_forward(x, w, bias=None, residual=None, activation="none", save="none
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
     N, dev = w.shape[0], x.get_device()
-    _like(w, torch.Size((N, K)), x.dtype, dev, "w")
-    shape = torch.Size((*x.shape[:-1], N))
+    _like(w, (N, K), x.dtype, dev, "w")
+    if N < 8 or N % 8:
+        raise ValueError(f"w must have a positive multiple of 8 rows, got {N}")
+    shape = (*x.shape[:-1], N)
     if bias is not None:
-        _like(bias, torch.Size((N,)), x.dtype, dev, "bias")
+        _like(bias, (N,), x.dtype, dev, "bias")
     if residual is not None:
         _like(residual, shape, x.dtype, dev, "residual")
-    n = instant_linear_workspace_bytes(M, N, K, dt)
-    ws = _workspace(n, x.device)
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    z = torch.empty_like(y) if save == "z" else None
-    z8 = _empty_ckpt(shape, x.device) if save == "z8" else None
-    q, s = z8 if z8 is not None else (None, None)
-    _ok(instant_linear_fwd(x, w, bias, residual, M, N, K, dt, act, y, z, q, s, ws, n), "instant_linear_fwd")
-    return y, z8 if z8 is not None else z
+    n = _fwd_bytes(M, N, K, dt)
+    ws, wp = _workspace(n, x)
+    y = x.new_empty(shape)
+    kept = z = q = s = None
+    if save == "z":
+        kept = torch.empty_like(y)
+        z = kept.data_ptr()
+    elif save == "z8":
+        kept = _empty_ckpt(shape, x)
+        q, s = kept.q.data_ptr(), kept.scale.data_ptr()
+    _ok(_lib.instant_linear_fwd(x.data_ptr(), w.data_ptr(), _p(bias), _p(residual), M, N, K, dt, act, y.data_ptr(), z,
+                                q, s, wp, n, _current(dev)), "instant_linear_fwd")
+    return y, kept
 
 
 def activation_backward(gy, z, activation="none", bias_grad=True):
@@ -232,28 +275,29 @@ def activation_backward(gy, z, activation="none", bias_grad=True):
     tensor like gy or a Checkpoint8 of its shape. With activation "none" gz is gy itself."""
     M, N, dt = _matrix(gy, "gy")
     act, dev = _act(activation), gy.get_device()
-    if not act and not bias_grad:
-        return gy, None
-    q = s = None
+    zp = q = s = None
     if not act:
         if z is not None:
             raise ValueError("activation 'none' takes no z")
+        if not bias_grad:
+            return gy, None
     elif isinstance(z, Checkpoint8):
         _ckpt(z, gy.shape, dev, "z")
-        q, s = z
-        z = None
+        q, s = z.q.data_ptr(), z.scale.data_ptr()
     elif z is None:
         raise ValueError(f"activation {activation!r} needs z")
     else:
         _like(z, gy.shape, gy.dtype, dev, "z")
+        zp = z.data_ptr()
     gz = torch.empty_like(gy) if act else None
-    gb = ws = None
+    gb = ws = wp = None
     n = 0
     if bias_grad:
-        gb = torch.empty(N, dtype=gy.dtype, device=gy.device)
-        n = instant_linear_workspace_bytes(M, N, 8, dt)
-        ws = _workspace(n, gy.device)
-    _ok(instant_act_bwd(gy, z, q, s, M, N, dt, act, gz, gb, ws, n), "instant_act_bwd")
+        gb = gy.new_empty(N)
+        n = _act_bytes(M, N, dt)
+        ws, wp = _workspace(n, gy)
+    _ok(_lib.instant_act_bwd(gy.data_ptr(), zp, q, s, M, N, dt, act, _p(gz), _p(gb), wp, n, _current(dev)),
+        "instant_act_bwd")
     return gz if act else gy, gb
 
 
@@ -266,22 +310,23 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
     K, dev = w.shape[1], gz.get_device()
-    _like(w, torch.Size((N, K)), gz.dtype, dev, "w")
-    shape = torch.Size((*gz.shape[:-1], K))
-    q = s = None
+    _like(w, (N, K), gz.dtype, dev, "w")
+    if K < 8 or K % 8:
+        raise ValueError(f"w must have a positive multiple of 8 columns, got {K}")
+    shape = (*gz.shape[:-1], K)
+    xp = q = s = None
     if isinstance(x, Checkpoint8):
         _ckpt(x, shape, dev, "x")
-        q, s = x
-        x = None
+        q, s = x.q.data_ptr(), x.scale.data_ptr()
     elif need_gw:
         _like(x, shape, gz.dtype, dev, "x")
-    else:
-        x = None
-    n = instant_linear_workspace_bytes(M, N, K, dt)
-    ws = _workspace(n, gz.device)
-    gx = torch.empty(shape, dtype=gz.dtype, device=gz.device) if need_gx else None
-    gw = torch.empty((N, K), dtype=gz.dtype, device=gz.device) if need_gw else None
-    _ok(instant_linear_bwd(gz, w, x, q, s, M, N, K, dt, gx, gw, ws, n), "instant_linear_bwd")
+        xp = x.data_ptr()
+    n = _bwd_bytes(M, N, K, dt)
+    ws, wp = _workspace(n, gz)
+    gx = gz.new_empty(shape) if need_gx else None
+    gw = torch.empty_like(w) if need_gw else None
+    _ok(_lib.instant_linear_bwd(gz.data_ptr(), w.data_ptr(), xp, q, s, M, N, K, dt, _p(gx), _p(gw), wp, n,
+                                _current(dev)), "instant_linear_bwd")
     return gx, gw
 
 
@@ -305,15 +350,18 @@ def rmsnorm_forward(x, weight, residual=None, eps=1e-6, y=True, y8=False) -> Nor
         raise ValueError("one of y and y8 has to be asked for")
     if not 0.0 <= eps < float("inf"):
         raise ValueError(f"eps must be finite and not negative, got {eps}")
-    _like(weight, torch.Size((C,)), x.dtype, dev, "weight")
+    _like(weight, (C,), x.dtype, dev, "weight")
     if residual is not None:
         _like(residual, x.shape, x.dtype, dev, "residual")
     h = torch.empty_like(x) if residual is not None else None
     out = torch.empty_like(x) if y else None
-    c = _empty_ckpt(x.shape, x.device) if y8 else None
-    q, s = c if c is not None else (None, None)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _ok(instant_rmsnorm_fwd(x, residual, weight, M, C, dt, eps, h, out, q, s, rstd), "instant_rmsnorm_fwd")
+    c = q = s = None
+    if y8:
+        c = _empty_ckpt(x.shape, x)
+        q, s = c.q.data_ptr(), c.scale.data_ptr()
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    _ok(_lib.instant_rmsnorm_fwd(x.data_ptr(), _p(residual), weight.data_ptr(), M, C, dt, eps, _p(h), _p(out), q, s,
+                                 rstd.data_ptr(), _current(dev)), "instant_rmsnorm_fwd")
     return NormOut(out, x if h is None else h, rstd, c)
 
 
@@ -324,16 +372,17 @@ def rmsnorm_backward(gy, h, weight, rstd, gh=None, need_gweight=True):
     M, C, dt = _matrix(gy, "gy")
     dev = gy.get_device()
     _like(h, gy.shape, gy.dtype, dev, "h")
-    _like(weight, torch.Size((C,)), gy.dtype, dev, "weight")
+    _like(weight, (C,), gy.dtype, dev, "weight")
     _like(rstd, gy.shape[:-1], torch.float32, dev, "rstd")
     if gh is not None:
         _like(gh, gy.shape, gy.dtype, dev, "gh")
     gx = torch.empty_like(gy)
-    gw = ws = None
+    gw = ws = wp = None
     n = 0
     if need_gweight:
-        gw = torch.empty(C, dtype=gy.dtype, device=gy.device)
-        n = instant_rmsnorm_workspace_bytes(M, C)
-        ws = _workspace(n, gy.device)
-    _ok(instant_rmsnorm_bwd(gy, h, weight, rstd, gh, M, C, dt, gx, gw, ws, n), "instant_rmsnorm_bwd")
+        gw = torch.empty_like(weight)
+        n = _norm_bytes(M, C)
+        ws, wp = _workspace(n, gy)
+    _ok(_lib.instant_rmsnorm_bwd(gy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _p(gh), M, C, dt,
+                                 gx.data_ptr(), _p(gw), wp, n, _current(dev)), "instant_rmsnorm_bwd")
     return gx, gw

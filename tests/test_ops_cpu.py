@@ -42,6 +42,10 @@ def test_workspace_sizes():
             n = ops.instant_linear_workspace_bytes(M, 4096, 1024, dt)
             assert n >= 256 and n % 256 == 0
             assert n < 1 << 31  # the partial sums' size does not grow with the batch
+            alone = [ops.instant_linear_fwd_workspace_bytes(M, 4096, 1024, dt),
+                     ops.instant_linear_bwd_workspace_bytes(M, 4096, 1024, dt),
+                     ops.instant_act_bwd_workspace_bytes(M, 4096, dt)]
+            assert max(alone) <= n
         n = ops.instant_rmsnorm_workspace_bytes(M, 65536)
         assert n >= 256 and n % 256 == 0
 
@@ -76,10 +80,10 @@ def test_act_bwd_refusals():
     for change in [dict(gy=None), dict(z=None), dict(z=A, zq=A, zs=A), dict(z=None, zq=A), dict(z=None, zs=A),
                    dict(gz=None), dict(act=0), dict(act=0, z=None, zq=A, zs=A), dict(gy=A + 8), dict(z=A + 8),
                    dict(gz=A + 8), dict(gb=A + 8), dict(M=-1), dict(N=0), dict(dtype=7), dict(act=9),
-                   dict(gb=A, ws=None), dict(gb=A, ws=W + 8)]:
+                   dict(gb=A, ws=None, M=1000), dict(gb=A, ws=W + 8, M=1000)]:
         assert act_bwd(**change) == E_ARG, change
     assert act_bwd(N=12) == E_SHAPE
-    assert act_bwd(gb=A, n=16) == E_SHAPE
+    assert act_bwd(gb=A, M=1000, n=16) == E_SHAPE
     assert act_bwd(M=0, gy=None, z=None) == OK
 
 
