@@ -1,0 +1,11 @@
+// The bfloat16 tile kernel (tile_kernel.hpp) for gx = gz w: A with k contiguous, B k-major.
+#include "tile_kernel.hpp"
+
+namespace instant {
+
+hipError_t launch_tile_bf16_gx(const Plan& p, const void* A, int lda, int M, const void* B, int ldb, int N, int K,
+                              const Epi& ep, float* part, hipStream_t st) {
+  return launch_planned<bf16, false, true>(p, A, lda, M, B, ldb, N, K, ep, part, st);
+}
+
+}  // namespace instant

@@ -258,8 +258,8 @@ hipError_t launch_ckpt_unpack(bool bf16_io, Ckpt c, int M, int C, void* x, hipSt
 
 // The three products of a layer with x [M][K], w [N][K], gz [M][N].
 enum class Prod { Fwd, Gx, Gw };
-// Floats of workspace one product needs.
-size_t linear_part_floats(bool bf16_io, Prod p, int M, int N, int K);
+// Floats of workspace one product needs (gw: with x as a checkpoint or in full).
+size_t linear_part_floats(bool bf16_io, Prod p, int M, int N, int K, bool x_ckpt);
 // Fwd: ep given. Gx: out [M][K]. Gw: out [N][K], x in full or (xc.q) as a checkpoint.
 hipError_t launch_linear_fwd(bool bf16_io, const void* x, const void* w, int M, int N, int K, const Epi& ep,
                              float* part, hipStream_t st);

@@ -40,9 +40,9 @@ instant_status sizes(int32_t M, std::initializer_list<int32_t> widths) {
   return INSTANT_OK;
 }
 
-size_t linear_fwd_bytes(bool bf, int M, int N, int K) { return 4 * linear_part_floats(bf, Prod::Fwd, M, N, K); }
-size_t linear_bwd_bytes(bool bf, int M, int N, int K) {
-  return 4 * std::max(linear_part_floats(bf, Prod::Gx, M, N, K), linear_part_floats(bf, Prod::Gw, M, N, K));
+size_t linear_fwd_bytes(bool bf, int M, int N, int K) { return 4 * linear_part_floats(bf, Prod::Fwd, M, N, K, false); }
+size_t linear_bwd_bytes(bool bf, int M, int N, int K, bool x_ckpt) {
+  return 4 * std::max(linear_part_floats(bf, Prod::Gx, M, N, K, false), linear_part_floats(bf, Prod::Gw, M, N, K, x_ckpt));
 }
 
 // A workspace that a call needs `need` bytes of (none: it may be null).
@@ -81,7 +81,7 @@ INSTANT_API instant_status instant_ckpt_unpack(const void* q, const void* scale,
 INSTANT_API size_t instant_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {
   if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
   const bool bf = dtype == INSTANT_BF16;
-  return align256(std::max({(size_t)256, linear_fwd_bytes(bf, M, N, K), linear_bwd_bytes(bf, M, N, K),
+  return align256(std::max({(size_t)256, linear_fwd_bytes(bf, M, N, K), linear_bwd_bytes(bf, M, N, K, true),
                             4 * act_bwd_part_floats(M, N)}));
 }
 
@@ -90,9 +90,9 @@ INSTANT_API size_t instant_linear_fwd_workspace_bytes(int32_t M, int32_t N, int3
   return linear_fwd_bytes(dtype == INSTANT_BF16, M, N, K);
 }
 
-INSTANT_API size_t instant_linear_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {
+INSTANT_API size_t instant_linear_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t x_ckpt) {
   if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
-  return linear_bwd_bytes(dtype == INSTANT_BF16, M, N, K);
+  return linear_bwd_bytes(dtype == INSTANT_BF16, M, N, K, x_ckpt != 0);
 }
 
 INSTANT_API size_t instant_act_bwd_workspace_bytes(int32_t M, int32_t N, int32_t dtype) {
@@ -137,7 +137,9 @@ INSTANT_API instant_status instant_linear_bwd(const void* gz, const void* w, con
   if ((xq == nullptr) != (xscale == nullptr) || (x && xq) || (M > 0 && !gx && !gw)) return INSTANT_E_ARG;
   if (M > 0 && (!gz || (gx && !w) || (gw && !x && !xq))) return INSTANT_E_ARG;
   const bool bf = dtype == INSTANT_BF16;
-  TRY(workspace_ok(workspace, workspace_bytes, linear_bwd_bytes(bf, M, N, K)));
+  TRY(workspace_ok(workspace, workspace_bytes,
+                   std::max(gx ? 4 * linear_part_floats(bf, Prod::Gx, M, N, K, false) : 0,
+                            gw ? 4 * linear_part_floats(bf, Prod::Gw, M, N, K, xq != nullptr) : 0)));
   hipError_t e = hipSuccess;
   if (gx && M > 0) e = launch_linear_gx(bf, gz, w, M, N, K, gx, (float*)workspace, S(stream));
   if (e == hipSuccess && gw)

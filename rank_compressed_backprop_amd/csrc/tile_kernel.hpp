@@ -1,12 +1,20 @@
-// The three products of a linear layer in bfloat16 on the matrix cores (the layouts and the
-// orientation are those of kernels_linear.hip; bf16 products are exact in the float32 sums).
+// The three products of a linear layer on the matrix cores, in bfloat16 (products exact, sums
+// float32) or float32 (v_mfma_f32_16x16x4_f32):
+//   fwd  y  [M][N]: A = x  [M][K] (k contiguous), B = w [N][K] (k contiguous)
+//   gx   gx [M][K]: A = gz [M][N] (k contiguous), B = w [N][K] (k-major: the contraction is N)
+//   gw   gw [N][K]: A = gz [M][N] (k-major: the contraction is M), B = x [M][K] (k-major)
+//
+// Orientation: the MFMA computes D[n][m] (the B operand takes the first slot). A lane receives
+// D rows 4 q + v (q = lane / 16, v < 4) of column m = lane % 16.
 //
 // Four waves share a block tile of BM x BN, one to a SIMD, so a wave tile is up to 128 x 128:
-// every operand byte read from LDS then feeds 128 products, and the LDS reads of a stage (64 k)
-// take half the matrix cores' time (a wave tile of 64 x 64 would take all of it).
+// every operand byte read from LDS then feeds 128 products, and the LDS reads of a stage (128
+// bytes of k: 64 bfloat16 or 32 float32)
+// take half the matrix cores' time in bfloat16 (a wave tile of 64 x 64 would take all of it; in
+// float32, at an eighth of the rate, LDS never matters).
 //
 // A stage goes from memory straight to LDS (16 bytes a lane); NS stages are held. A wave runs
-// two half stages of 32 k by turns from two sets of operand registers:
+// two half stages by turns from two sets of operand registers:
 //   multiply half 0 of stage s   while half 1 of s is read from LDS
 //   wait for stage s + 1, barrier: every wave has read all of s
 //   multiply half 1 of stage s   while half 0 of s + 1 is read and stage s + NS is requested
@@ -24,13 +32,11 @@
 #include "dma.hpp"
 #include "lds_tiles.hpp"
 #include "ops.hpp"
-#include "tile16.hpp"
+#include "tile.hpp"
 
 namespace instant {
 
 namespace {
-
-constexpr int K16 = 64;  // k per stage
 
 // 16 bytes per lane from base + off (base uniform) straight into LDS at lds_wave + 16 * lane.
 __device__ __forceinline__ void lds_dma16_at(const void* base, unsigned off, void* lds_wave) {
@@ -44,27 +50,42 @@ __device__ __forceinline__ void keep_in_agprs(f32x4& v) {
 #endif
 }
 
-// One operand of a block tile: W rows (columns of the k-major layout) of a stage in LDS.
-//   k contiguous: W rows of 128 bytes; chunk c (16 bytes) of row r at c ^ (r & 7)
-//   k-major     : 64 k rows of 2 W bytes; chunk c of row r at c ^ swizzle(r)
-// PAIR: the operand of the first slot (columns n). In the k-contiguous layout LDS row
-// 32 p + 16 hh + i holds operand row 32 p + 8 (i / 4) + 4 hh + i % 4, so its reads are those of
-// the other operand; the k-major layout permutes as it is read (lds_tiles.hpp).
-template <bool KMAJ, bool PAIR, int W>
+// One operand of a block tile: W rows (columns of the k-major layout) of a stage in LDS, in
+// chunks of 16 bytes.
+//   k contiguous: W rows of 128 bytes; chunk c of row r at c ^ (r & 7)
+//   k-major     : KS k rows of W elements; chunk c of row r at c ^ swizzle(r)
+// PAIR: the operand of the first slot (columns n): its 16-row tiles 2 p and 2 p + 1 hold the 32
+// columns of pair p so that a lane receives 8 consecutive ones, row i of tile hh being column
+// 8 (i / 4) + 4 hh + i % 4 of the pair. In the k-contiguous layout LDS row 32 p + 16 hh + i holds
+// that operand row, so its reads are those of the other operand; the k-major layout permutes as
+// it is read (bfloat16: lds_tiles.hpp, whose halves alternate).
+template <class T, bool KMAJ, bool PAIR, int W>
 struct Side {
-  static constexpr int BYTES = W * K16 * 2;
+  typedef typename MM<T>::frag frag;
+  static constexpr int ES = sizeof(T), CE = 16 / ES;  // bytes of an element, elements of a chunk
+  static constexpr int KS = 128 / ES;                 // k per stage
+  static constexpr int BYTES = W * 128;
   static constexpr int LOADS = BYTES / 4096;  // of 1024 bytes, for each of the four waves
-  static constexpr int CPR = KMAJ ? W / 8 : 8;  // chunks a row
+  static constexpr int CPR = KMAJ ? W / CE : 8;  // chunks a row
+  static_assert(W % 32 == 0 && (!PAIR || W % 64 == 0), "the swizzles stay within a row");
   // k contiguous: byte offsets of this lane's rows; k-major: of its column chunks
   unsigned off[LOADS];
-  unsigned kb;  // bytes of one k row (k-major)
+  unsigned kb;  // bytes between stored rows
   int chunk;    // k contiguous: the logical chunk of all its loads (their rows differ by 32s)
   unsigned at;  // and its offset in the stage being requested
 
   __device__ static __forceinline__ int swz(int r) {
-    if constexpr (!KMAJ) return r & 7;
-    const int flip = W % 128 ? 7 : 15;  // (the flip of chunk bit 3 needs rows of whole 16 chunks)
-    return (PAIR ? kswz_b(r) : kswz_a(r)) & flip;
+    if constexpr (!KMAJ) {
+      return r & 7;
+    } else if constexpr (ES == 2) {
+      // (a flip of a chunk bit needs rows of whole powers of two of chunks above it)
+      constexpr int flip = W % 128 == 0 ? 15 : W % 64 == 0 ? 7 : 3;
+      return (PAIR ? kswz_b(r) : kswz_a(r)) & flip;
+    } else {
+      // a read takes 16 columns of rows 4 q + g, q < 4: rows of odd q use the banks that those of
+      // even q leave (PAIR: every other chunk of eight; else four chunks side by side)
+      return ((r >> 2) & 1) * (PAIR ? 1 : 4);
+    }
   }
   // LDS row and logical chunk of this lane's load j
   __device__ static __forceinline__ void place(int j, int wave, int lane, int& r, int& c) {
@@ -78,32 +99,32 @@ struct Side {
   }
 
   __device__ __forceinline__ void init(int first, int rows, int ld, int wave, int lane) {
-    kb = 2u * (unsigned)ld;
+    kb = ES * (unsigned)ld;
     chunk = (lane & 7) ^ ((lane >> 3) & 7);
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       int r, c;
       place(j, wave, lane, r, c);
-      if constexpr (KMAJ) off[j] = 2u * (unsigned)min(8 * c, rows - 8 - first);  // rows % 8 == 0
+      if constexpr (KMAJ) off[j] = ES * (unsigned)min(CE * c, rows - CE - first);  // rows % 8 == 0
       else off[j] = (unsigned)min(row_of(r), rows - 1 - first) * kb;
     }
   }
   // the tile's first element at stage k0
-  __device__ static __forceinline__ const bf16* origin(const bf16* p, int first, int ld, int k0) {
+  __device__ static __forceinline__ const T* origin(const T* p, int first, int ld, int k0) {
     return KMAJ ? p + (size_t)k0 * ld + first : p + (size_t)first * ld + k0;
   }
-  // a stage of which `left` >= 1 k are there (64 or more: all of it; k contiguous: a multiple of
+  // a stage of which `left` >= 1 k are there (KS or more: all of it; k contiguous: a multiple of
   // 8) is requested next
   __device__ __forceinline__ void stage(int left) {
-    if constexpr (!KMAJ) at = 16u * (unsigned)min(chunk, (left >> 3) - 1);
+    if constexpr (!KMAJ) at = 16u * (unsigned)min(chunk, left / CE - 1);
   }
   // load j of the stage at `base`
-  __device__ __forceinline__ void issue(int j, const bf16* base, int left, unsigned char* lds, int wave, int lane) const {
+  __device__ __forceinline__ void issue(int j, const T* base, int left, unsigned char* lds, int wave, int lane) const {
     unsigned o = at + off[j];
     if constexpr (KMAJ) {
       int r, c;
       place(j, wave, lane, r, c);
-      o = __umul24((unsigned)min(r, left - 1), kb) + off[j];  // (kb < 2^20)
+      o = __umul24((unsigned)min(r, left - 1), kb) + off[j];  // (kb <= 2^20)
     }
     lds_dma16_at(base, o, lds + 1024 * (j * 4 + wave));
   }
@@ -112,25 +133,30 @@ struct Side {
     each<LOADS>([&](auto j) {
       int r, c;
       place(j, wave, lane, r, c);
-      if (KMAJ ? r >= left : 8 * chunk >= left)
+      if (KMAJ ? r >= left : CE * chunk >= left)
         *reinterpret_cast<f32x4*>(lds + 1024 * (j * 4 + wave) + 16 * lane) = zero4();
     });
   }
-  // LDS reads that make one MFMA operand, and read `part` of the operand of 16-row tile `t` (first
-  // row 16 t of the tile), k half h
-  static constexpr int PARTS = KMAJ ? 2 : 1;
-  __device__ static __forceinline__ void read(bf16x8& f, int part, const unsigned char* lds, int t, int h, int lane) {
+  // LDS reads that make one MFMA operand (16 bytes: the k of one k-step that the lane supplies),
+  // and read `part` of the operand of 16-row tile `t` (first row 16 t of the tile), k half h
+  static constexpr int PARTS = !KMAJ ? 1 : ES == 2 ? 2 : 4;
+  __device__ static __forceinline__ void read(frag& f, int part, const unsigned char* lds, int t, int h, int lane) {
+    const int q = lane >> 4, s = lane & 15;
     if constexpr (!KMAJ) {
-      const int r = 16 * t + (lane & 15);
-      f = *reinterpret_cast<const bf16x8*>(lds + r * 128 + 16 * ((4 * h + (lane >> 4)) ^ (r & 7)));
-    } else {
-      const int q = lane >> 4, s = lane & 15, a = s & 3;
+      const int r = 16 * t + s;
+      f = *reinterpret_cast<const frag*>(lds + r * 128 + 16 * ((4 * h + q) ^ (r & 7)));
+    } else if constexpr (ES == 2) {
+      const int a = s & 3;
       const int col0 = PAIR ? 32 * (t >> 1) : 16 * t;
       const int col = PAIR ? col0 + 8 * a + 4 * ((t & 1) ^ (a & 1)) : col0 + 4 * a;
       const int r0 = 32 * h + 8 * q + (s >> 2);  // and row r0 + 4, which has the same swizzle
       const bf16x4 v = tr_read(lds + (r0 + 4 * part) * (2 * W) + 16 * ((col >> 3) ^ swz(r0)) + (col & 7) * 2);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[4 * part + j] = v[j];
+    } else {
+      const int col = PAIR ? 32 * (t >> 1) + 8 * (s >> 2) + 4 * (t & 1) + (s & 3) : 16 * t + s;
+      const int r = 16 * h + 4 * q + part;
+      f[part] = *reinterpret_cast<const float*>(lds + r * (4 * W) + 16 * ((col >> 2) ^ swz(r)) + (col & 3) * 4);
     }
   }
 };
@@ -139,17 +165,20 @@ struct Side {
 
 // C(m, n) = sum_k A(m, k) B(n, k) over k slice blockIdx.z. WM x WN: 16-row tiles of a wave
 // (WN even); the waves form a 2 x 2 grid. Grid (tiles, 1, S).
-template <bool AKM, bool BKM, int WM, int WN, int NS, bool PART>
-__global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__ A, int lda, int M,
-                                                        const bf16* __restrict__ B, int ldb, int N, int K, Epi ep,
-                                                        float* __restrict__ part) {
+template <class T, bool AKM, bool BKM, int WM, int WN, int NS, bool PART>
+__global__ __launch_bounds__(256, 1) void tile_kernel(const T* __restrict__ A, int lda, int M, const T* __restrict__ B,
+                                                      int ldb, int N, int K, Epi ep, float* __restrict__ part,
+                                                      bool add) {
+  typedef typename MM<T>::frag frag;
+  typedef typename MM<T>::vec8 vec8;
   constexpr int BM = 32 * WM, BN = 32 * WN;
-  typedef Side<AKM, false, BM> SA;
-  typedef Side<BKM, true, BN> SB;
+  typedef Side<T, AKM, false, BM> SA;
+  typedef Side<T, BKM, true, BN> SB;
+  constexpr int KS = SA::KS;
   constexpr int STAGE = SA::BYTES + SB::BYTES;
   // rows a wave turns at a time at the end, and the floats of one (4 more than its columns, for
   // the banks)
-  constexpr int ROWS = WM == 8 ? 64 : 32, LDO = 16 * WN + 4;
+  constexpr int ROWS = WM == 8 ? 64 : WM == 1 ? 16 : 32, LDO = 16 * WN + 4;
   constexpr int TURN = 4 * ROWS * LDO * 4;
   __shared__ __attribute__((aligned(1024))) unsigned char ring[NS * STAGE > TURN ? NS * STAGE : TURN];
   const int lane = threadIdx.x & (WAVE - 1);
@@ -158,8 +187,8 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   int tm, tn;
   tile_of(xcd_unit(blockIdx.x, mt * nt), mt, nt, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  const int nst = (K + K16 - 1) / K16, S = gridDim.z, z = blockIdx.z;
-  const int s0 = (int)((unsigned)nst * z / S), nq = (int)((unsigned)nst * (z + 1) / S) - s0;  // (nst <= 2^20)
+  const int nst = (K + KS - 1) / KS, S = gridDim.z, z = blockIdx.z;
+  const int s0 = (int)((unsigned)nst * z / S), nq = (int)((unsigned)nst * (z + 1) / S) - s0;  // (nst <= 2^21)
   const int wm = wave >> 1, wn = wave & 1;
 
   SA sa;
@@ -167,12 +196,12 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   sa.init(m0, M, lda, wave, lane);
   sb.init(n0, N, ldb, wave, lane);
   // the next stage to request
-  const bf16* pa = SA::origin(A, m0, lda, s0 * K16);
-  const bf16* pb = SB::origin(B, n0, ldb, s0 * K16);
-  const size_t da = AKM ? (size_t)K16 * lda : K16, db = BKM ? (size_t)K16 * ldb : K16;
+  const T* pa = SA::origin(A, m0, lda, s0 * KS);
+  const T* pb = SB::origin(B, n0, ldb, s0 * KS);
+  const size_t da = AKM ? (size_t)KS * lda : KS, db = BKM ? (size_t)KS * ldb : KS;
   // k from that stage to the slice's end
-  int left = min(K, (s0 + nq) * K16) - s0 * K16;
-  const int tail = (left - 1) % K16 + 1;  // k of the slice's last stage
+  int left = min(K, (s0 + nq) * KS) - s0 * KS;
+  const int tail = (left - 1) % KS + 1;  // k of the slice's last stage
   sa.stage(left);
   sb.stage(left);
   constexpr int NDMA = SA::LOADS + SB::LOADS;
@@ -181,10 +210,10 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
     else sb.issue(j - SA::LOADS, pb, left, st + SA::BYTES, wave, lane);
   };
   auto advance = [&] {  // (the last stage stays)
-    const bool more = left > K16;
+    const bool more = left > KS;
     pa += more ? da : 0;
     pb += more ? db : 0;
-    left -= more ? K16 : 0;
+    left -= more ? KS : 0;
     sa.stage(left);
     sb.stage(left);
   };
@@ -194,7 +223,7 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   for (int i = 0; i < WM; ++i)
 #pragma unroll
     for (int j = 0; j < WN; ++j) acc[i][j] = zero4();
-  bf16x8 fa[2][WM], fb[2][WN];
+  frag fa[2][WM], fb[2][WN];
   constexpr int NMMA = WM * WN, NRB = WN * SB::PARTS, NREAD = NRB + WM * SA::PARTS;
   auto read = [&](auto r, auto set, const unsigned char* st) {  // LDS read r of half `set`
     if constexpr (r < NRB) {
@@ -211,7 +240,7 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   auto half = [&](auto set, auto to, auto dma, const unsigned char* st, unsigned char* slot) {
     constexpr int ND = decltype(dma)::value ? NDMA : 0, NE = NREAD + ND;
     each<NMMA>([&](auto t) {
-      acc[t / WN][t % WN] = MM<bf16>::mma(fb[set][t % WN], fa[set][t / WN], acc[t / WN][t % WN]);
+      acc[t / WN][t % WN] = MM<T>::mma(fb[set][t % WN], fa[set][t / WN], acc[t / WN][t % WN]);
       each<NE>([&](auto e) {
         if constexpr (e * NMMA / NE == t) {
           constexpr int d = e * ND / NE;  // requests before event e
@@ -224,7 +253,7 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   };
   // stage s has arrived for this wave: clear what lies behind the contraction's end
   auto arrived = [&](int s, unsigned char* st) {
-    if (tail < K16 && s == nq - 1) {
+    if (tail < KS && s == nq - 1) {
       sa.clear(tail, st, wave, lane);
       sb.clear(tail, st + SA::BYTES, wave, lane);
       __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -268,20 +297,20 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
   bare_barrier();  // every wave is done with the ring
   float* mine = reinterpret_cast<float*>(ring) + wave * ROWS * LDO;
   const int q4 = lane >> 4, l16 = lane & 15;
-  // the k-major layout's halves alternate: this lane's first four columns of a pair are in tile
+  // the bfloat16 k-major layout's halves alternate: this lane's first four columns of a pair are in tile
   // q4 % 2 of it (lds_tiles.hpp)
-  const int lo = BKM && (q4 & 1) ? 4 : 0;
+  const int lo = BKM && sizeof(T) == 2 && (q4 & 1) ? 4 : 0;
   // lane -> row of a batch's RPI rows and 8 of its columns; four neighbouring lanes hold a group
   // of 32 columns. NB batches at a time, so that their loads, exponentials and stores overlap.
   constexpr int UPR = 2 * WN, RPI = WAVE / UPR, NB = 4;
   const int row = lane / UPR, col = lane % UPR, n = n0 + 16 * WN * wn + 8 * col;
   float bias[8];
-  if constexpr (!PART) load_bias<bf16>(ep, n, N, bias);
-  auto fetch_res = [&](bf16x8 (&r)[NB], int mr) {
+  if constexpr (!PART) load_bias<T>(ep, n, N, bias);
+  auto fetch_res = [&](vec8 (&r)[NB], int mr) {
     if (ep.res)
       each<NB>([&](auto k) {
         const int m = mr + k * RPI;
-        if (m < M && n < N) r[k] = *reinterpret_cast<const bf16x8*>((const bf16*)ep.res + (size_t)m * N + n);
+        if (m < M && n < N) r[k] = *reinterpret_cast<const vec8*>((const T*)ep.res + (size_t)m * N + n);
       });
   };
   each<WM * 16 / ROWS>([&](auto c) {
@@ -292,7 +321,7 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
       });
     });
     const int mb = m0 + 16 * WM * wm + ROWS * c + row;
-    bf16x8 r[NB];
+    vec8 r[NB];
     if constexpr (!PART) fetch_res(r, mb);
 #pragma unroll 1
     for (int it = 0; it < ROWS; it += RPI * NB) {
@@ -305,13 +334,20 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
       });
       if constexpr (PART) {
         each<NB>([&](auto k) {
-          if (in[k]) store_row<float, 8>(part + ((size_t)z * M + mb + it + k * RPI) * N + n, v[k]);
+          if (!in[k]) return;
+          float* p = part + ((size_t)z * M + mb + it + k * RPI) * N + n;
+          if (add) {
+            float o[8];
+            load8(p, o);
+            each<8>([&](auto j) { v[k][j] += o[j]; });
+          }
+          store_row<float, 8>(p, v[k]);
         });
       } else {
-        bf16x8 rc[NB];
+        vec8 rc[NB];
         each<NB>([&](auto k) { rc[k] = r[k]; });
         if (it + RPI * NB < ROWS) fetch_res(r, mb + it + RPI * NB);  // before this batch's stores
-        epilogue<bf16, NB, 1, 2>(ep, bias, rc, v, mb + it, RPI, n, N, in);
+        epilogue<T, NB, 1, 2>(ep, bias, rc, v, mb + it, RPI, n, N, in);
       }
     }
   });
@@ -319,35 +355,38 @@ __global__ __launch_bounds__(256, 1) void tile16_kernel(const bf16* __restrict__
 
 namespace {
 
-template <bool AKM, bool BKM, int WM, int WN, int NS>
-hipError_t go16(const bf16* A, int lda, int M, const bf16* B, int ldb, int N, int K, const Epi& ep, int S, float* part,
-                hipStream_t st) {
+template <class T, bool AKM, bool BKM, int WM, int WN, int NS>
+hipError_t run_tile(const Plan& p, const T* A, int lda, int M, const T* B, int ldb, int N, int K, const Epi& ep,
+                    float* part, hipStream_t st) {
   const unsigned tiles = (unsigned)((M + 32 * WM - 1) / (32 * WM)) * ((N + 32 * WN - 1) / (32 * WN));
-  if (S > 1)
-    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, NS, true>), dim3(tiles, 1, S), dim3(256), 0, st, A, lda, M, B, ldb,
-                       N, K, ep, part);
+  if (p.S < 1 || p.S > (K + 128 / (int)sizeof(T) - 1) / (128 / (int)sizeof(T))) return hipErrorInvalidValue;
+  if (p.part)
+    hipLaunchKernelGGL((tile_kernel<T, AKM, BKM, WM, WN, NS, true>), dim3(tiles, 1, p.S), dim3(256), 0, st, A, lda, M,
+                       B, ldb, N, K, ep, part, p.add);
   else
-    hipLaunchKernelGGL((tile16_kernel<AKM, BKM, WM, WN, NS, false>), dim3(tiles), dim3(256), 0, st, A, lda, M, B, ldb, N, K,
-                       ep, part);
+    hipLaunchKernelGGL((tile_kernel<T, AKM, BKM, WM, WN, NS, false>), dim3(tiles), dim3(256), 0, st, A, lda, M, B, ldb,
+                       N, K, ep, part, false);
   return hipGetLastError();
 }
 
-// The launch for one pair of layouts (each layout is compiled in a file of its own).
-template <bool AKM, bool BKM>
-hipError_t launch16(const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep, float* part,
-                    hipStream_t st) {
-  const Plan16 p = plan16(M, N, K);
-#define GO(WM, WN, NS)                  \
+// The launch for one type and pair of layouts (each compiled in a file of its own).
+template <class T, bool AKM, bool BKM>
+hipError_t launch_planned(const Plan& p, const void* A, int lda, int M, const void* B, int ldb, int N, int K,
+                          const Epi& ep, float* part, hipStream_t st) {
+#define GO(WM, WN, NS)                        \
   if (p.wm == WM && p.wn == WN && p.ns == NS) \
-    return go16<AKM, BKM, WM, WN, NS>((const bf16*)A, lda, M, (const bf16*)B, ldb, N, K, ep, p.S, part, st)
+    return run_tile<T, AKM, BKM, WM, WN, NS>(p, (const T*)A, lda, M, (const T*)B, ldb, N, K, ep, part, st)
   GO(8, 8, 2);
-  GO(8, 6, 2);
   GO(4, 4, 2);
-  GO(4, 4, 4);
-  GO(2, 4, 3);
-  GO(2, 4, 2);
   GO(2, 2, 2);
-  GO(2, 2, 4);
+  GO(1, 2, 4);
+  if constexpr (sizeof(T) == 2) {
+    GO(8, 6, 2);
+    GO(4, 4, 4);
+    GO(2, 4, 3);
+    GO(2, 4, 2);
+    GO(2, 2, 4);
+  }
 #undef GO
   return hipErrorInvalidValue;
 }

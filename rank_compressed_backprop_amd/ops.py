@@ -30,7 +30,7 @@ _sig = {
     "instant_ckpt_unpack": (_st, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "instant_linear_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "instant_linear_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
-    "instant_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "instant_act_bwd_workspace_bytes": (_sz, [_i, _i, _i]),
     "instant_linear_fwd": (_st, [_vp] * 4 + [_i] * 5 + [_vp] * 5 + [_sz, _vp]),
     "instant_act_bwd": (_st, [_vp] * 4 + [_i] * 4 + [_vp] * 3 + [_sz, _vp]),
@@ -65,8 +65,8 @@ def instant_linear_fwd_workspace_bytes(M, N, K, dtype) -> int:
     return int(_lib.instant_linear_fwd_workspace_bytes(M, N, K, dtype))
 
 
-def instant_linear_bwd_workspace_bytes(M, N, K, dtype) -> int:
-    return int(_lib.instant_linear_bwd_workspace_bytes(M, N, K, dtype))
+def instant_linear_bwd_workspace_bytes(M, N, K, dtype, x_ckpt) -> int:
+    return int(_lib.instant_linear_bwd_workspace_bytes(M, N, K, dtype, int(x_ckpt)))
 
 
 def instant_act_bwd_workspace_bytes(M, N, dtype) -> int:
@@ -321,7 +321,7 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
     elif need_gw:
         _like(x, shape, gz.dtype, dev, "x")
         xp = x.data_ptr()
-    n = _bwd_bytes(M, N, K, dt)
+    n = _bwd_bytes(M, N, K, dt, q is not None)
     ws, wp = _workspace(n, gz)
     gx = gz.new_empty(shape) if need_gx else None
     gw = torch.empty_like(w) if need_gw else None

@@ -631,6 +631,31 @@ def test_offsets_past_32_bits():
     assert torch.equal(bits(gx[-200:]), bits(gx2))
 
 
+@pytest.mark.parametrize("dtype,M,K", [(BF, 16500, 8192), (FP, 8250, 8192), (BF, 33000, 8192)])
+def test_weight_gradient_in_chunks(dtype, M, K):
+    """Checkpoints whose values in full pass the workspace's 256 MB: gw adds up over chunks of
+    rows, the last of them short."""
+    import rank_compressed_backprop_amd as rcb
+    from rank_compressed_backprop_amd import ops
+    N = 24
+    code = rcb.INSTANT_BF16 if dtype == BF else rcb.INSTANT_FP32
+    assert M * K * (2 if dtype == BF else 4) > 256 << 20
+    assert ops.instant_linear_bwd_workspace_bytes(M, N, K, code, True) < 512 << 20
+    g = gen("chunks", M)
+    x = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(M)).to(dtype)
+    gz = randn(g, M, N, dtype=dtype)
+    c = ops.checkpoint_pack(x)
+    _, gw = ops.linear_backward(gz, torch.zeros(N, K, dtype=dtype, device="cuda"), c, need_gx=False)
+    _, again = ops.linear_backward(gz, torch.zeros(N, K, dtype=dtype, device="cuda"), c, need_gx=False)
+    assert torch.equal(bits(gw), bits(again))
+    d = gz.double().t().contiguous()
+    ref = mag = 0
+    for m in range(0, M, 4096):
+        v = value64(ops.Checkpoint8(c.q[m:m + 4096], c.scale[m:m + 4096]))
+        ref, mag = ref + d[:, m:m + 4096] @ v, mag + d[:, m:m + 4096].abs() @ v.abs()
+    within("gw", gw, ref, U[dtype] * ref.abs() + 1.01 * GAMMA(M) * mag + 1e-38)
+
+
 def test_wrong_arguments_raise():
     from rank_compressed_backprop_amd import ops
     x, w = torch.zeros(4, 64, dtype=BF, device="cuda"), torch.zeros(32, 64, dtype=BF, device="cuda")

@@ -43,7 +43,8 @@ def test_workspace_sizes():
             assert n >= 256 and n % 256 == 0
             assert n < 1 << 31  # the partial sums' size does not grow with the batch
             alone = [ops.instant_linear_fwd_workspace_bytes(M, 4096, 1024, dt),
-                     ops.instant_linear_bwd_workspace_bytes(M, 4096, 1024, dt),
+                     ops.instant_linear_bwd_workspace_bytes(M, 4096, 1024, dt, True),
+                     ops.instant_linear_bwd_workspace_bytes(M, 4096, 1024, dt, False),
                      ops.instant_act_bwd_workspace_bytes(M, 4096, dt)]
             assert max(alone) <= n
         n = ops.instant_rmsnorm_workspace_bytes(M, 65536)
