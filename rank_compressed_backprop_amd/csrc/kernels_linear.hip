@@ -51,6 +51,11 @@ namespace {
 // over 1024 8.5 against 31 us; against a fixed 64 x 64 tile: 16384 x 1024 over 4096 108 against 197
 // us. In float32 the matrix cores have an eighth of the rate, nothing else holds them up, and four
 // shapes do.
+//
+// An epilogue with an activation or a checkpoint (`heavy`: up to 60 operations a value) costs
+// tiles that have a compute unit to themselves more: nothing runs beside it. (bfloat16 with
+// GELU and an 8-bit pre-activation, 256 x 192 against 128 x 128 tiles: 16384 x 768 over 768 35.5
+// against 33.0 us, without them 26.3 against 27.7; 6272 x 1792 over 448 29.9 against 25.3 us.)
 struct Shape {
   int wm, wn, ns, fit;
   float lone, each, ends;
@@ -64,17 +69,18 @@ constexpr Shape SHAPES_FP32[] = {{8, 8, 2, 1, 1.0f, 7.5f, 7.9f},
                                  {2, 2, 2, 4, 0.62f, 0.505f, 1.26f},
                                  {1, 2, 4, 3, 0.37f, 0.29f, 1.1f}};
 
-template <int NSH> Plan choose(const Shape (&shapes)[NSH], int nst, int M, int N) {
+template <int NSH> Plan choose(const Shape (&shapes)[NSH], int nst, int M, int N, bool heavy) {
   static constexpr int slices[] = {1, 2, 3, 4, 6, 8, 12, 16};
   Plan best{0, 0, 0, 1, false, false};
   float least = 0.0f;
   for (const Shape& s : shapes) {
+    const float ends = s.ends * (!heavy ? 1.0f : s.fit == 1 ? 3.5f : 2.0f);
     const long tiles = (((long)M + 32 * s.wm - 1) / (32 * s.wm)) * (((long)N + 32 * s.wn - 1) / (32 * s.wn));
     for (int S : slices) {
       if (S > 1 && (tiles * S > 2048 || nst < 2 * S)) break;
       const long n = (tiles * S + 255) / 256;  // blocks of the busiest compute unit
       const int nq = (nst + S - 1) / S;
-      auto group = [&](int k) { return nq * std::max(s.lone, k * s.each) + s.ends * (0.5f + 0.5f * k); };
+      auto group = [&](int k) { return nq * std::max(s.lone, k * s.each) + ends * (0.5f + 0.5f * k); };
       const int rest = (int)(n % s.fit);
       float t = (float)(n / s.fit) * group(s.fit) + (rest ? group(rest) : 0.0f);
       if (S > 1) t += 2.6f + 0.1f * S + (float)S * M * N * 8.0f / 6.5e6f;
@@ -87,8 +93,8 @@ template <int NSH> Plan choose(const Shape (&shapes)[NSH], int nst, int M, int N
   return best;
 }
 
-Plan plan(bool bf16_io, int M, int N, int K) {
-  return bf16_io ? choose(SHAPES_BF16, (K + 63) / 64, M, N) : choose(SHAPES_FP32, (K + 31) / 32, M, N);
+Plan plan(bool bf16_io, int M, int N, int K, bool heavy) {
+  return bf16_io ? choose(SHAPES_BF16, (K + 63) / 64, M, N, heavy) : choose(SHAPES_FP32, (K + 31) / 32, M, N, heavy);
 }
 
 template <class T>
@@ -102,7 +108,7 @@ hipError_t sum_parts(const Plan& p, const float* part, int M, int N, const Epi& 
 template <class T>
 hipError_t run(TileLaunch launch, const void* A, int lda, int M, const void* B, int ldb, int N, int K, const Epi& ep,
                float* part, hipStream_t st) {
-  const Plan p = plan(sizeof(T) == 2, M, N, K);
+  const Plan p = plan(sizeof(T) == 2, M, N, K, ep.act != ACT_NONE || ep.zc.q);
   if (p.part && !part) return hipErrorInvalidValue;
   const hipError_t e = launch(p, A, lda, M, B, ldb, N, K, ep, part, st);
   return e == hipSuccess && p.part ? sum_parts<T>(p, part, M, N, ep, st) : e;
@@ -132,7 +138,7 @@ hipError_t run_gw8(TileLaunch launch, const T* gz, Ckpt x, int M, int N, int K, 
     const hipError_t e = launch_ckpt_unpack(BF, x, M, K, ws, st);
     return e == hipSuccess ? run<T>(launch, gz, N, N, ws, K, K, M, ep, part, st) : e;
   }
-  Plan p = plan(BF, N, K, rows);
+  Plan p = plan(BF, N, K, rows, false);
   const int S = p.S;
   p.part = true;
   for (int m = 0; m < M; m += rows) {
@@ -161,7 +167,8 @@ size_t linear_part_floats(bool bf16_io, Prod p, int M, int N, int K, bool x_ckpt
     chunks = k < M;
     n = unpacked_floats(bf16_io, k, K);
   }
-  const int S = plan(bf16_io, a, b, k).S;
+  int S = plan(bf16_io, a, b, k, false).S;
+  if (p == Prod::Fwd) S = std::max(S, plan(bf16_io, a, b, k, true).S);  // whatever its epilogue
   return n + (S > 1 || chunks ? (size_t)S * a * b : 0);
 }
 

@@ -51,16 +51,20 @@ __device__ __forceinline__ float ck_scale(unsigned byte) { return __builtin_bit_
 // its inverse (byte <= 249 for finite groups, so the exponent field stays normal)
 __device__ __forceinline__ float ck_inv_scale(unsigned byte) { return __builtin_bit_cast(float, (254u - byte) << 23); }
 
-// Eight values to int8 (nearest, ties to even): packed low to high.
+// Eight values to int8 (nearest, ties to even): packed low to high. The product with the scale's
+// inverse is exact, and adding 1.5 * 2^23 (where a float's step is 1) rounds it to the nearest
+// integer, whose low byte is the float's: one operation a value, and the packing.
 __device__ __forceinline__ uint2 ck_quant8(const float v[8], unsigned byte) {
   const float inv = ck_inv_scale(byte == 255u ? 254u : byte);
+  unsigned t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = __builtin_bit_cast(unsigned, fmaf(v[j], inv, 12582912.0f));
   unsigned r[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    unsigned p = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p |= ((unsigned)(int)__builtin_rintf(v[4 * h + j] * inv) & 0xffu) << (8 * j);
-    r[h] = byte == 255u ? 0u : p;
+    const unsigned lo = __builtin_amdgcn_perm(t[4 * h + 1], t[4 * h], 0x0c0c0400u);
+    const unsigned hi = __builtin_amdgcn_perm(t[4 * h + 3], t[4 * h + 2], 0x04000c0cu);
+    r[h] = byte == 255u ? 0u : lo | hi;
   }
   return uint2{r[0], r[1]};
 }
@@ -131,7 +135,7 @@ template <int ACT, bool FAST> __device__ __forceinline__ float act_fwd(float z) 
     return z * phi<FAST>(z, e);
   }
   if constexpr (ACT == ACT_GELU_TANH) {  // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-    const float u2 = 2.0f * GT_C * z * fmaf(GT_A * z, z, 1.0f);
+    const float u2 = z * fmaf(2.0f * GT_C * GT_A, z * z, 2.0f * GT_C);
     return z * inv1<FAST>(1.0f + ex<FAST>(-u2));
   }
   if constexpr (ACT == ACT_SILU) return z * inv1<FAST>(1.0f + ex<FAST>(-z));
@@ -199,31 +203,44 @@ template <class T> __device__ __forceinline__ void load_bias(const Epi& ep, int 
 }
 
 // The eight consecutive columns n .. n+7 (n % 8 == 0) of rows m, m + step, ... (NB of them, each
-// `in` the output or not): their bias, their residuals r (anything without one) and their sums v,
-// which are used up. The four lanes that differ in lane-id bits X1, X2 hold the 32-column group
-// of n and must all call.
+// `in` the output or not; `all` when the compiler may take every lane's as in, which a whole tile
+// of the output says): their bias (zeros without one), their residuals r (anything without) and
+// their sums v, which are used up. The four lanes that differ in lane-id bits X1, X2 hold the
+// 32-column group of n and must all call.
 template <class T, int NB, int X1, int X2>
 __device__ __forceinline__ void epilogue(const Epi& ep, const float bias[8], const typename MM<T>::vec8 (&r)[NB],
-                                         float (&v)[NB][8], int m, int step, int n, int N, const bool (&in)[NB]) {
+                                         float (&v)[NB][8], int m, int step, int n, int N, const bool (&in)[NB],
+                                         bool all) {
   constexpr bool FAST = sizeof(T) == 2;
+  const size_t at = (size_t)m * N + n, down = (size_t)step * N;
+  auto store = [&](T* p) {
+    if (all) {
 #pragma unroll
-  for (int k = 0; k < NB; ++k)
+      for (int k = 0; k < NB; ++k) store_row<T, 8>(p + k * down, v[k]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[k][j] += bias[j];
+      for (int k = 0; k < NB; ++k)
+        if (in[k]) store_row<T, 8>(p + k * down, v[k]);
+    }
+  };
+  if (ep.bias) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] += bias[j];
+  }
   if (ep.zc.q) {
+    const size_t G = ck_groups(N), g = (size_t)m * G + n / CK_GROUP;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const unsigned byte = ck_scale_byte(ck_group_amax<X1, X2>(v[k], in[k]));
       if (in[k]) {
-        const size_t row = m + k * step;
-        *reinterpret_cast<uint2*>(ep.zc.q + row * N + n) = ck_quant8(v[k], byte);
-        if (n % CK_GROUP == 0) ep.zc.scale[row * ck_groups(N) + n / CK_GROUP] = (uint8_t)byte;
+        *reinterpret_cast<uint2*>(ep.zc.q + at + k * down) = ck_quant8(v[k], byte);
+        if (n % CK_GROUP == 0) ep.zc.scale[g + k * step * G] = (uint8_t)byte;
       }
     }
   } else if (ep.z) {
-#pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (in[k]) store_row<T, 8>((T*)ep.z + (size_t)(m + k * step) * N + n, v[k]);
+    store((T*)ep.z + at);
   }
   act_fwd_all<FAST, NB>(ep.act, v);
   if (ep.res) {
@@ -232,9 +249,7 @@ __device__ __forceinline__ void epilogue(const Epi& ep, const float bias[8], con
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] += (float)r[k][j];
   }
-#pragma unroll
-  for (int k = 0; k < NB; ++k)
-    if (in[k]) store_row<T, 8>((T*)ep.y + (size_t)(m + k * step) * N + n, v[k]);
+  store((T*)ep.y + at);
 }
 
 // One row of it.
@@ -248,7 +263,7 @@ __device__ __forceinline__ void epilogue8(const Epi& ep, float (&v)[8], int m, i
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[0][j] = v[j];
   const bool ok[1] = {in};
-  epilogue<T, 1, X1, X2>(ep, bias, r, w, m, 0, n, N, ok);
+  epilogue<T, 1, X1, X2>(ep, bias, r, w, m, 0, n, N, ok, false);
 }
 
 // ---- host launchers (each returns the launch status; pointers are device pointers)

@@ -302,8 +302,10 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(const T* __restrict__ A, i
   const int lo = BKM && sizeof(T) == 2 && (q4 & 1) ? 4 : 0;
   // lane -> row of a batch's RPI rows and 8 of its columns; four neighbouring lanes hold a group
   // of 32 columns. NB batches at a time, so that their loads, exponentials and stores overlap.
-  constexpr int UPR = 2 * WN, RPI = WAVE / UPR, NB = 4;
+  constexpr int UPR = 2 * WN, RPI = WAVE / UPR, NB = ROWS / RPI < 4 ? ROWS / RPI : 4;
   const int row = lane / UPR, col = lane % UPR, n = n0 + 16 * WN * wn + 8 * col;
+  // every lane has rows and columns in every batch, and they lie in the output
+  const bool whole = ROWS % (RPI * NB) == 0 && WAVE % UPR == 0 && m0 + BM <= M && n0 + BN <= N;
   float bias[8];
   if constexpr (!PART) load_bias<T>(ep, n, N, bias);
   auto fetch_res = [&](vec8 (&r)[NB], int mr) {
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(const T* __restrict__ A, i
         vec8 rc[NB];
         each<NB>([&](auto k) { rc[k] = r[k]; });
         if (it + RPI * NB < ROWS) fetch_res(r, mb + it + RPI * NB);  // before this batch's stores
-        epilogue<T, NB, 1, 2>(ep, bias, rc, v, mb + it, RPI, n, N, in);
+        epilogue<T, NB, 1, 2>(ep, bias, rc, v, mb + it, RPI, n, N, in, whole);
       }
     }
   });
