@@ -363,7 +363,9 @@ namespace {
 template <class T, bool AKM, bool BKM, int WM, int WN, int NS>
 hipError_t run_tile(const Plan& p, const T* A, int lda, int M, const T* B, int ldb, int N, int K, const Epi& ep,
                     float* part, hipStream_t st) {
-  const unsigned tiles = (unsigned)((M + 32 * WM - 1) / (32 * WM)) * ((N + 32 * WN - 1) / (32 * WN));
+  const size_t all = (size_t)((M + 32 * WM - 1) / (32 * WM)) * ((N + 32 * WN - 1) / (32 * WN));
+  if (all > 0xffffffu) return hipErrorInvalidValue;  // (a launch takes 2^32 threads: an output of 2^38 or more)
+  const unsigned tiles = (unsigned)all;
   if (p.S < 1 || p.S > (K + 128 / (int)sizeof(T) - 1) / (128 / (int)sizeof(T))) return hipErrorInvalidValue;
   if (p.part)
     hipLaunchKernelGGL((tile_kernel<T, AKM, BKM, WM, WN, NS, true>), dim3(tiles, 1, p.S), dim3(256), 0, st, A, lda, M,
