@@ -63,8 +63,8 @@ struct Shape {
 };
 constexpr Shape SHAPES_BF16[] = {
     {8, 8, 2, 1, 1.21f, 1.17f, 8.4f},  {8, 6, 2, 1, 1.01f, 0.91f, 7.4f},   {4, 4, 2, 2, 0.47f, 0.356f, 2.14f},
-    {4, 4, 4, 1, 0.43f, 0.25f, 3.0f},  {2, 4, 3, 2, 0.33f, 0.253f, 2.67f}, {2, 4, 2, 3, 0.505f, 0.34f, 1.74f},
-    {2, 2, 2, 4, 0.43f, 0.204f, 0.84f}, {2, 2, 4, 2, 0.05f, 0.192f, 1.91f}, {1, 2, 4, 3, 0.07f, 0.176f, 1.13f}};
+    {4, 4, 4, 1, 0.43f, 0.25f, 3.0f},  {2, 4, 3, 2, 0.33f, 0.253f, 2.67f}, {2, 2, 2, 4, 0.43f, 0.204f, 0.84f},
+    {2, 2, 4, 2, 0.05f, 0.192f, 1.91f}, {1, 2, 4, 3, 0.07f, 0.176f, 1.13f}};
 constexpr Shape SHAPES_FP32[] = {{8, 8, 2, 1, 1.0f, 7.5f, 7.9f},
                                  {4, 4, 2, 2, 2.16f, 1.9f, 2.8f},
                                  {2, 2, 2, 4, 0.62f, 0.505f, 1.26f},

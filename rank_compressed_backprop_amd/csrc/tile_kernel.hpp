@@ -391,7 +391,6 @@ hipError_t launch_planned(const Plan& p, const void* A, int lda, int M, const vo
     GO(8, 6, 2);
     GO(4, 4, 4);
     GO(2, 4, 3);
-    GO(2, 4, 2);
     GO(2, 2, 4);
   }
 #undef GO

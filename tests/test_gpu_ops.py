@@ -198,6 +198,55 @@ def test_linear_forward_workload_sizes(shape):
     check_forward(ops, M, N, K, BF, "gelu", True, True, "z8")
 
 
+# Sizes that reach every tile shape and ring depth of every product, with the contraction whole and
+# split, with edges inside a tile: (rows, columns, contraction) of the output.
+EVERY_TILE = {
+    ("fwd", BF): [(1, 8, 1168), (1, 8, 80), (2897, 8, 1952), (1, 8, 8), (486, 368, 2480), (471, 1096, 352),
+                  (422, 2832, 5256), (747, 1360, 1032), (1643, 584, 1768), (10175, 280, 8), (2736, 424, 3320),
+                  (1518, 1416, 1720), (3762, 1344, 5384), (19654, 544, 232), (1656, 7912, 616)],
+    ("gx", BF): [(1, 8, 1328), (1, 8, 72), (9018, 8, 2480), (1, 8, 8), (459, 360, 2416), (1382, 328, 280),
+                 (186, 2768, 3736), (1398, 864, 960), (1126, 920, 2136), (1063, 1968, 208), (985, 1312, 2928),
+                 (3748, 560, 1464), (7152, 576, 3680), (1711, 4728, 896), (3629, 1040, 4976), (5338, 2360, 680)],
+    ("gw", BF): [(8, 8, 1110), (8, 8, 67), (5824, 8, 3326), (8, 8, 1), (680, 200, 2230), (1720, 264, 257),
+                 (424, 1464, 3985), (1392, 744, 925), (848, 1408, 2125), (5464, 528, 6), (776, 1608, 2933),
+                 (1560, 1448, 1470), (1232, 2192, 8012), (3632, 2248, 758), (6456, 656, 4537), (6128, 2144, 641)],
+    ("fwd", FP): [(3, 8, 296), (1, 8, 8), (450, 344, 1104), (9399, 8, 8), (1700, 1520, 2304), (910, 3280, 8),
+                  (1702, 7384, 32)],
+    ("gx", FP): [(1, 8, 312), (1, 8, 8), (774, 152, 1280), (9355, 8, 8), (736, 3208, 2112), (3466, 856, 8),
+                 (4128, 1224, 3144), (14689, 872, 16)],
+    ("gw", FP): [(8, 8, 295), (8, 8, 1), (504, 376, 895), (8480, 16, 1), (728, 3288, 3420), (8696, 336, 1),
+                 (6432, 728, 5541), (7808, 1568, 1)],
+}
+
+
+@pytest.mark.parametrize("which", EVERY_TILE, ids=lambda w: f"{w[0]}-{'bf16' if w[1] == BF else 'fp32'}")
+def test_every_tile(which):
+    from rank_compressed_backprop_amd import ops
+    kind, dtype = which
+    for i, (a, b, k) in enumerate(EVERY_TILE[which]):
+        print(f"[tile] {kind} {dtype} {a} x {b} over {k}", flush=True)
+        if kind == "fwd":
+            for act, save in (("none", "none"), ("silu", "z8"), ("relu", "z")):
+                check_forward(ops, a, b, k, dtype, act, bool(i % 2), bool(i % 3), save)
+            continue
+        g = gen("tile", which[0], str(dtype), a, b, k)
+        M, N, K = (a, k, b) if kind == "gx" else (k, a, b)
+        gz, w = randn(g, M, N, dtype=dtype), randn(g, N, K, dtype=dtype)
+        d, u = gz.double(), U[dtype]
+        if kind == "gx":
+            gx, _ = ops.linear_backward(gz, w, None, need_gw=False)
+            ref, mag = d @ w.double(), d.abs() @ w.double().abs()
+            within("gx", gx, ref, u * ref.abs() + (1 + u) * GAMMA(N) * mag + 1e-38)
+        else:
+            x = randn(g, M, K, dtype=dtype)
+            d = d.t().contiguous()
+            for xx, x64 in ((x, x.double()), (ops.checkpoint_pack(x), None)):
+                x64 = value64(xx) if x64 is None else x64
+                _, gw = ops.linear_backward(gz, w, xx, need_gx=False)
+                ref, mag = d @ x64, d.abs() @ x64.abs()
+                within("gw", gw, ref, u * ref.abs() + (1 + u) * GAMMA(M) * mag + 1e-38)
+
+
 def test_linear_forward_nonfinite_stays():
     """An infinity or NaN in one row reaches that row's outputs, and no other row's."""
     from rank_compressed_backprop_amd import ops
