@@ -319,15 +319,15 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(const T* __restrict__ A, i
       });
   };
   each<WM * 16 / ROWS>([&](auto c) {
+    const int mb = m0 + 16 * WM * wm + ROWS * c + row;
+    vec8 r[NB];
+    if constexpr (!PART) fetch_res(r, mb);  // (in flight while the rows are turned)
     each<ROWS / 16>([&](auto i) {
       each<WN>([&](auto j) {
         *reinterpret_cast<f32x4*>(mine + (16 * i + l16) * LDO + 32 * (j / 2) + 8 * q4 + ((j & 1) ? 4 - lo : lo)) =
             acc[c * (ROWS / 16) + i][j];
       });
     });
-    const int mb = m0 + 16 * WM * wm + ROWS * c + row;
-    vec8 r[NB];
-    if constexpr (!PART) fetch_res(r, mb);
 #pragma unroll 1
     for (int it = 0; it < ROWS; it += RPI * NB) {
       float v[NB][8];
