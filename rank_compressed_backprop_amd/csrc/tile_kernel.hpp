@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(const T* __restrict__ A, i
 
   // Out through LDS: each wave turns ROWS rows of its tile at a time, so that the epilogue is one
   // small loop over 8 columns a lane with whole rows stored by neighbouring lanes. (Unrolled over
-  // the accumulators it was 100 KB of code, fetched cold by every block: 15 us of a block's time.)
+  // the accumulators it was 100 KB of code: 16384 x 768 -> 768 in 256 x 256 tiles 44.8 us, so 31.6.)
   bare_barrier();  // every wave is done with the ring
   float* mine = reinterpret_cast<float*>(ring) + wave * ROWS * LDO;
   const int q4 = lane >> 4, l16 = lane & 15;
