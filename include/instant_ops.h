@@ -70,9 +70,10 @@ instant_status instant_ckpt_pack(const void* x, int32_t M, int32_t C, int32_t dt
 instant_status instant_ckpt_unpack(const void* q, const void* scale, int32_t M, int32_t C, int32_t dtype, void* x,
                                    void* stream);
 
-/* Bytes of workspace for instant_linear_fwd, instant_act_bwd and instant_linear_bwd with these
- * sizes (0 if the sizes are not accepted; at least 256 otherwise): partial sums of a split
- * contraction, and for gw from a checkpoint up to 256 MB of x's values at a time. */
+/* Bytes of workspace that are enough for each of instant_linear_fwd, instant_act_bwd and
+ * instant_linear_bwd (x in full or as a checkpoint) with these sizes (0 if the sizes are not
+ * accepted; at least 256 otherwise): partial sums of a split contraction, and for gw from a
+ * checkpoint up to 256 MB of x's values at a time. */
 size_t instant_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype);
 
 /* What each of the three calls needs alone, the backward with x as a checkpoint (x_ckpt != 0) or

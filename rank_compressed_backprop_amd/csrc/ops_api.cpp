@@ -82,7 +82,7 @@ INSTANT_API size_t instant_linear_workspace_bytes(int32_t M, int32_t N, int32_t 
   if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
   const bool bf = dtype == INSTANT_BF16;
   return align256(std::max({(size_t)256, linear_fwd_bytes(bf, M, N, K), linear_bwd_bytes(bf, M, N, K, true),
-                            4 * act_bwd_part_floats(M, N)}));
+                            linear_bwd_bytes(bf, M, N, K, false), 4 * act_bwd_part_floats(M, N)}));
 }
 
 INSTANT_API size_t instant_linear_fwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {

@@ -2,6 +2,7 @@
 exported, and what a call may not be is refused on the host before anything is enqueued."""
 import ctypes
 import os
+import random
 import re
 
 import pytest
@@ -154,3 +155,18 @@ def test_tensor_functions_refuse_cpu_tensors_and_bad_shapes():
             call()
     with pytest.raises(TypeError):
         ops.checkpoint_unpack(ops.Checkpoint8(x, x), torch.float16)
+
+
+def test_one_workspace_serves_every_call():
+    """What instant_linear_workspace_bytes returns is enough for each of the three calls, whichever
+    way x is given: a checkpoint is split by chunks of rows, x in full by all of them, so either may
+    need more."""
+    rng = random.Random(5)
+    sizes = [(19142, 3504, 10672, BF), (6613, 3984, 10496, FP), (368011, 456, 18920, BF), (368011, 456, 18920, FP)]
+    for _ in range(4000):
+        M = int(2 ** rng.uniform(0, 26))
+        sizes.append((M, 8 * int(2 ** rng.uniform(0, 12)), 8 * int(2 ** rng.uniform(0, 12)), rng.choice([BF, FP])))
+    for s in sizes:
+        alone = [ops.instant_linear_fwd_workspace_bytes(*s), ops.instant_act_bwd_workspace_bytes(s[0], s[1], s[3]),
+                 *(ops.instant_linear_bwd_workspace_bytes(*s, ckpt) for ckpt in (False, True))]
+        assert max(alone) <= ops.instant_linear_workspace_bytes(*s), (s, alone)
