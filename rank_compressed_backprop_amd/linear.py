@@ -92,6 +92,7 @@ class _FusedLinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @ops.differentiated_once
     def backward(ctx, gy):
         w, *kept = ctx.saved_tensors
         mod, mode, n = ctx.mod, ctx.mode, ctx.n_kept
@@ -124,6 +125,9 @@ class InstantLinear(torch.nn.Module):
     rounding of at most 1/127 of a group's largest value (x enters g_w, the pre-activation the
     activation's slope). A norm that writes its output in 8 bits (norm.InstantRMSNorm) hands
     that over as x8, and nothing is packed here. The low-rank steps keep x_hat as ever.
+
+    The library's backward passes cannot be differentiated again: with any of these options a
+    backward pass with create_graph=True raises RuntimeError.
 
     dtype is the library's I/O dtype ("bf16" or "fp32"); inputs and the weight must have
     it. N_cal calibration steps start every window of N_t steps (N_cal <= N_t).

@@ -21,6 +21,7 @@ class _RMSNormFn(torch.autograd.Function):
         return out.y, out.h if ctx.has_res else None, q, s
 
     @staticmethod
+    @ops.differentiated_once
     def backward(ctx, gy, gh, *_):
         h, weight, rstd = ctx.saved_tensors
         if gy is None:  # only h was used
@@ -36,7 +37,8 @@ class InstantRMSNorm(torch.nn.Module):
 
     forward(x, residual=None) returns ops.NormOut's y and h: (y, h) with a residual, where
     h = x + residual is the new residual stream, else y. With checkpoint="int8" a Checkpoint8 of
-    y follows, for InstantLinear's x8."""
+    y follows, for InstantLinear's x8. The gradients cannot be differentiated again (create_graph=True
+    raises RuntimeError)."""
 
     def __init__(self, C, eps=1e-6, dtype="bf16", checkpoint=None, device="cuda"):
         super().__init__()

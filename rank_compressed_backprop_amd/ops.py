@@ -183,6 +183,18 @@ def _act(name):
     return code
 
 
+def differentiated_once(backward):
+    """Decorator of a layer's backward pass on these operators. Its results have no graph, so a
+    second derivative would silently lack the layer's terms: create_graph=True (which runs
+    backward passes with gradients enabled) is refused."""
+    @functools.wraps(backward)
+    def checked(ctx, *grads):
+        if torch.is_grad_enabled():
+            raise RuntimeError("the backward pass of this layer cannot be differentiated again (create_graph=True)")
+        return backward(ctx, *grads)
+    return checked
+
+
 # ----------------------------------------------------------------------------- checkpoints
 
 class Checkpoint8(NamedTuple):

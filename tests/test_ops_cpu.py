@@ -4,6 +4,7 @@ import ctypes
 import os
 import random
 import re
+import types
 
 import pytest
 
@@ -170,3 +171,30 @@ def test_one_workspace_serves_every_call():
         alone = [ops.instant_linear_fwd_workspace_bytes(*s), ops.instant_act_bwd_workspace_bytes(s[0], s[1], s[3]),
                  *(ops.instant_linear_bwd_workspace_bytes(*s, ckpt) for ckpt in (False, True))]
         assert max(alone) <= ops.instant_linear_workspace_bytes(*s), (s, alone)
+
+
+def test_layers_refuse_second_derivatives(monkeypatch):
+    """The backward passes are launches without a graph: a second derivative would be short of
+    their terms, so it is refused. Plain forms stand in for the kernels here."""
+    from rank_compressed_backprop_amd.linear import _FusedLinearFn
+    from rank_compressed_backprop_amd.norm import _RMSNormFn
+    raw = torch.no_grad()
+    monkeypatch.setattr(ops, "linear_forward", raw(lambda x, w, b, r, act, save: (
+        torch.relu(x @ w.t() + b) + r, x @ w.t() + b)))
+    monkeypatch.setattr(ops, "activation_backward", raw(lambda gy, z, act, bias_grad: (
+        gy * (z > 0), (gy * (z > 0)).sum((0, 1)))))
+    monkeypatch.setattr(ops, "linear_backward", raw(lambda gz, w, x, need_gx, need_gw: (
+        gz @ w, gz.flatten(0, 1).t() @ x.flatten(0, 1))))
+    monkeypatch.setattr(ops, "rmsnorm_forward", raw(lambda x, w, r, eps, y8: ops.NormOut(
+        (x + r) * w, x + r, torch.ones(x.shape[:-1]), None)))
+    monkeypatch.setattr(ops, "rmsnorm_backward", raw(lambda gy, h, w, rstd, gh, need: (gy * w, (gy * h).sum((0, 1)))))
+    g = torch.Generator().manual_seed(3)
+    x, r, b, n, w = (torch.randn(*s, generator=g).requires_grad_(True)
+                     for s in ((2, 3, 8), (2, 3, 8), (8,), (8,), (8, 8)))
+    layer = types.SimpleNamespace(checkpoint=None, activation="relu")
+    for leaves, call in [((x, w, b, r), lambda: _FusedLinearFn.apply(x, w, b, r, None, None, layer, "exact")),
+                         ((x, n, r), lambda: _RMSNormFn.apply(x, r, n, 1e-6, False)[0])]:
+        torch.autograd.grad(call().square().sum(), leaves)  # once is what they are for
+        for loss in (call().square().sum(), call().sum()):  # the incoming gradient with and without a graph
+            with pytest.raises(RuntimeError, match="differentiated again"):
+                torch.autograd.grad(loss, leaves, create_graph=True)
