@@ -13,11 +13,15 @@
  * A checkpoint in 8 bits of a matrix [M, C] is
  *   q      int8  [M, C]
  *   scale  uint8 [M, ceil(C / 32)]   one biased power-of-two exponent per 32 channels of a row
- * and stands for q * 2^(scale - 127). The exponent is the smallest of 1 .. 254 with
+ * and stands for q * 2^(scale - 127). The exponent is the smallest of 1 .. 248 with
  * max |value| <= 127 * 2^(scale - 127), and q the nearest integer (ties to even), so an element
  * is off by at most half a step, 2^(scale - 128) <= max |group| / 127. |q| <= 127 takes 7 bits:
- * every value a checkpoint stands for is exact in bfloat16. A group that holds a NaN or an
- * infinity has scale 255 and stands for NaN throughout, so a fault is not hidden.
+ * every value a checkpoint stands for is finite and exact in bfloat16. At the ends of float's
+ * range: a group whose largest is above 127 * 2^121 (the last 1/128 of the largest binade) has
+ * scale 248, and elements above that are kept as it, at most a step (2^121 < max |group| / 127)
+ * off; a group whose largest is below 63.5 * 2^-126 has scale 1, and half a step is 2^-127 there.
+ * A group that holds a NaN or an infinity has scale 255 and stands for NaN throughout, so a fault
+ * is not hidden.
  *
  * Conventions (where they differ from instant.h it is said so)
  *   - Pointers are device pointers of the current device, aligned to 16 bytes (scale and rstd:

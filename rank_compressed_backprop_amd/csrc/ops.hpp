@@ -40,25 +40,33 @@ __device__ __forceinline__ unsigned mag_bits(float v) { return __builtin_bit_cas
 
 // The biased exponent of a group's scale from the magnitude bits of its largest element: the
 // smallest power of two s with amax <= 127 s. 127 = 1.984375 * 2^6, so an amax with mantissa
-// field above 0x7e0000 needs one exponent more: the addition carries exactly then.
+// field above 0x7e0000 needs one exponent more: the addition carries exactly then. At most 248:
+// 64 steps of the next would be 2^128, no float.
+constexpr unsigned CK_MAX_SCALE = 248;
 __device__ __forceinline__ unsigned ck_scale_byte(unsigned amax) {
   if (amax >= 0x7f800000u) return 255u;
   const int b = (int)((amax + 0x01ffffu) >> 23) - 6;
-  return (unsigned)(b < 1 ? 1 : b);
+  return (unsigned)(b < 1 ? 1 : b > (int)CK_MAX_SCALE ? (int)CK_MAX_SCALE : b);
 }
 // 2^(byte - 127); the float of byte 255 is infinity, and such a group's q is 0: 0 * inf = NaN.
 __device__ __forceinline__ float ck_scale(unsigned byte) { return __builtin_bit_cast(float, byte << 23); }
-// its inverse (byte <= 249 for finite groups, so the exponent field stays normal)
+// its inverse (byte <= 248 for finite groups, so the exponent field stays normal)
 __device__ __forceinline__ float ck_inv_scale(unsigned byte) { return __builtin_bit_cast(float, (254u - byte) << 23); }
 
 // Eight values to int8 (nearest, ties to even): packed low to high. The product with the scale's
 // inverse is exact, and adding 1.5 * 2^23 (where a float's step is 1) rounds it to the nearest
-// integer, whose low byte is the float's: one operation a value, and the packing.
+// integer, whose low byte is the float's: one operation a value, and the packing. Only at the
+// largest scale can that be 128 steps (from above 127.5, at the end of float's range): those
+// become 127, in a branch of their own, as the others need no limit.
 __device__ __forceinline__ uint2 ck_quant8(const float v[8], unsigned byte) {
   const float inv = ck_inv_scale(byte == 255u ? 254u : byte);
   unsigned t[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) t[j] = __builtin_bit_cast(unsigned, fmaf(v[j], inv, 12582912.0f));
+  if (byte == CK_MAX_SCALE) {  // (as integers the floats' bits differ by the steps)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = min(max(t[j], 0x4b400000u - 127u), 0x4b400000u + 127u);
+  }
   unsigned r[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -134,6 +134,37 @@ def test_checkpoint_edges():
             assert torch.equal(v[~want.cuda()], torch.ones_like(v[~want.cuda()]))
 
 
+def test_checkpoint_ends_of_the_range():
+    """Finite values stay finite: 127 steps of 2^121 are the largest that a checkpoint stands for,
+    and what lies above is off by at most a step. The smallest step is 2^-126."""
+    from rank_compressed_backprop_amd import ops
+    top = 127 * 2.0 ** 121
+    for dtype in (BF, FP):
+        most = torch.finfo(dtype).max
+        rows = [[most, -most, top, -top, 1e38, 2.0 ** 121, 2.0 ** 120, 1.5 * 2.0 ** 121],
+                [-most] * 8, [most] + [0.0] * 7, [top, 126.5 * 2.0 ** 121, -125.5 * 2.0 ** 121, 1.0],
+                [2.0 ** -126, 2.0 ** -127, -2.0 ** -127, 2.0 ** -128, 1.5 * 2.0 ** -126, 63 * 2.0 ** -126]]
+        x = torch.zeros(len(rows), 72, dtype=torch.float64)
+        for i, r in enumerate(rows):
+            x[i, 32:32 + len(r)] = torch.tensor(r, dtype=torch.float64)
+        x = x.to(dtype).cuda()
+        w = torch.eye(72, dtype=dtype, device="cuda")
+        packed = ops.checkpoint_pack(x)
+        # the product with 1 gives the same values, and so the same checkpoint
+        _, kept = ops.linear_forward(x, w, save="z8")
+        assert torch.equal(packed.q[:4], kept.q[:4]) and torch.equal(packed.scale[:4], kept.scale[:4])
+        assert packed.scale[:, 1].tolist() == [248, 248, 248, 248, 1]
+        v = ops.checkpoint_unpack(packed, dtype).double()
+        assert bool(torch.isfinite(v).all())
+        assert torch.equal(v, value64(packed))
+        x64 = x.double()
+        assert torch.equal(v[:4].abs() == top, x64[:4].abs() > 126.5 * 2.0 ** 121)
+        step = torch.where(x64.abs() > top, 2.0 ** 121, 2.0 ** 120)
+        step[4] = 2.0 ** -127
+        assert bool(((v - x64).abs() <= step).all())
+        assert bool(((v - x64)[:4].abs() <= x64[:4].abs().amax(1, keepdim=True) / 127).all())
+
+
 # ------------------------------------------------------------------------- linear, forward
 
 def check_forward(ops, M, N, K, dtype, act, bias, res, save, key=0):
