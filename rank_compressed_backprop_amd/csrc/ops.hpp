@@ -105,7 +105,7 @@ __device__ __forceinline__ unsigned ck_group_amax(const float v[8], bool in) {
 }
 
 // ---- activations (float32). FAST takes the hardware's exp and reciprocal (1 ulp each) and is
-// used for bfloat16 outputs, whose own rounding is 2^-9.
+// used for bfloat16 outputs, whose own rounding is up to 2^-8 of the value.
 
 template <bool FAST> __device__ __forceinline__ float ex(float v) {
   return FAST ? __builtin_amdgcn_exp2f(v * 1.44269504088896341f) : expf(v);
@@ -114,22 +114,25 @@ template <bool FAST> __device__ __forceinline__ float inv1(float v) {
   return FAST ? __builtin_amdgcn_rcpf(v) : 1.0f / v;
 }
 
-// Phi(z), the normal distribution function. FAST: erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2),
-// t = 1 / (1 + p x), x >= 0 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26;
-// absolute error below 1.5e-7); `e` receives exp(-z^2 / 2).
+// Phi(z), the normal distribution function; `e` receives exp(-z^2 / 2). FAST: Phi(-x) =
+// t (c1 + t (c2 + ...)) exp(-x^2 / 2) with t = 1 / (1 + p x), x >= 0, p and the six coefficients
+// fitted to the least largest error up to x = 13.2, where the exponential leaves float's normal
+// range: evaluated in float32 it is within 2.6e-7, and within 2.1e-5 of the value, so that GELU is
+// rounded once in its tail too. (A fit of the absolute error alone is off by 0.4% of the value at
+// z = -6 and by 3% at -12.)
 template <bool FAST> __device__ __forceinline__ float phi(float z, float& e) {
   e = ex<FAST>(-0.5f * z * z);
   if constexpr (!FAST) {
     return 0.5f * erfcf(-z * 0.70710678118654752f);
   } else {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float half = 0.5f * p * t * e;  // Phi(-|z|)
-    return z < 0.0f ? half : 1.0f - half;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.2972787f, fabsf(z), 1.0f));
+    float p = fmaf(-0.08200984f, t, 0.23852773f);
+    p = fmaf(p, t, -0.040558513f);
+    p = fmaf(p, t, 0.15472628f);
+    p = fmaf(p, t, 0.1101131f);
+    p = fmaf(p, t, 0.11920107f);
+    const float low = p * t * e;  // Phi(-|z|)
+    return z < 0.0f ? low : 1.0f - low;
   }
 }
 

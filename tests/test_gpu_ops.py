@@ -366,6 +366,31 @@ def test_slopes_far_out():
             assert bool(((gz.float() - want)[0][fine].abs() <= U[dtype] * 1.13 + 2.0 ** -19 * 200).all()), (act, gz)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("act,low", [("gelu", -12.5), ("gelu_tanh", -9.5), ("silu", -80.0)])
+def test_activation_tails(act, low, dtype):
+    """Far below zero an activation and its slope are small, and still right relative to their
+    value. An exponential's argument of up to 88 is built in up to four roundings of 2^-24, 2.1e-5
+    of the value, and the distribution function is fitted to 2.1e-5: together within 2^-14, beside
+    the output's own rounding."""
+    from rank_compressed_backprop_amd import ops
+    z = torch.linspace(low, -1.5, 4096).reshape(512, 8).to(dtype).cuda()  # (below the slopes' zeros)
+    y, _ = ops.linear_forward(z, torch.eye(8, dtype=dtype, device="cuda"), activation=act)
+    gz, _ = ops.activation_backward(torch.ones_like(z), z, act)
+    z64 = z.double()
+    if act == "gelu":
+        y64 = z64 * 0.5 * torch.erfc(-z64 / 2 ** 0.5)
+        s64 = 0.5 * torch.erfc(-z64 / 2 ** 0.5) + z64 * torch.exp(-z64 ** 2 / 2) / (2 * np.pi) ** 0.5
+    else:  # z sigmoid(v), whose terms do not cancel
+        c = 2 * (2 / np.pi) ** 0.5
+        v = z64 if act == "silu" else c * (z64 + 0.044715 * z64 ** 3)
+        dv = 1.0 if act == "silu" else c * (1 + 3 * 0.044715 * z64 ** 2)
+        s = torch.sigmoid(v)
+        y64, s64 = z64 * s, s + z64 * s * (1 - s) * dv
+    for name, got, ref in (("y", y, y64), ("slope", gz, s64)):
+        within(f"{act} {name}", got, ref, (U[dtype] + (1 + U[dtype]) * 2.0 ** -14) * ref.abs())
+
+
 # ------------------------------------------------------------------------- RMS norm
 
 NORM_SHAPES = [(1, 8), (1, 4096), (3, 40), (5, 512), (4, 520), (2, 1032), (301, 768), (9, 2048), (7, 2056), (6, 4104),
