@@ -81,10 +81,12 @@ instant_status instant_ckpt_unpack(const void* q, const void* scale, int32_t M, 
 size_t instant_linear_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype);
 
 /* What each of the three calls needs alone, the backward with x as a checkpoint (x_ckpt != 0) or
- * in full (0: nothing, the workspace may be NULL; also where the
- * sizes are not accepted, which the call itself reports). */
+ * in full (x_ckpt 0), for both gradients or for one of them (0: nothing, the workspace may be
+ * NULL; also where the sizes are not accepted, which the call itself reports). */
 size_t instant_linear_fwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype);
 size_t instant_linear_bwd_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t x_ckpt);
+size_t instant_linear_gx_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype);
+size_t instant_linear_gw_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t x_ckpt);
 size_t instant_act_bwd_workspace_bytes(int32_t M, int32_t N, int32_t dtype);
 
 /* y = act(x w^T + bias) + res. bias and res may be NULL; res may be y itself. The

@@ -41,8 +41,12 @@ instant_status sizes(int32_t M, std::initializer_list<int32_t> widths) {
 }
 
 size_t linear_fwd_bytes(bool bf, int M, int N, int K) { return 4 * linear_part_floats(bf, Prod::Fwd, M, N, K, false); }
+size_t linear_gx_bytes(bool bf, int M, int N, int K) { return 4 * linear_part_floats(bf, Prod::Gx, M, N, K, false); }
+size_t linear_gw_bytes(bool bf, int M, int N, int K, bool x_ckpt) {
+  return 4 * linear_part_floats(bf, Prod::Gw, M, N, K, x_ckpt);
+}
 size_t linear_bwd_bytes(bool bf, int M, int N, int K, bool x_ckpt) {
-  return 4 * std::max(linear_part_floats(bf, Prod::Gx, M, N, K, false), linear_part_floats(bf, Prod::Gw, M, N, K, x_ckpt));
+  return std::max(linear_gx_bytes(bf, M, N, K), linear_gw_bytes(bf, M, N, K, x_ckpt));
 }
 
 // A workspace that a call needs `need` bytes of (none: it may be null).
@@ -95,6 +99,16 @@ INSTANT_API size_t instant_linear_bwd_workspace_bytes(int32_t M, int32_t N, int3
   return linear_bwd_bytes(dtype == INSTANT_BF16, M, N, K, x_ckpt != 0);
 }
 
+INSTANT_API size_t instant_linear_gx_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype) {
+  if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
+  return linear_gx_bytes(dtype == INSTANT_BF16, M, N, K);
+}
+
+INSTANT_API size_t instant_linear_gw_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t x_ckpt) {
+  if (sizes(M, {N, K}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
+  return linear_gw_bytes(dtype == INSTANT_BF16, M, N, K, x_ckpt != 0);
+}
+
 INSTANT_API size_t instant_act_bwd_workspace_bytes(int32_t M, int32_t N, int32_t dtype) {
   if (sizes(M, {N}) != INSTANT_OK || !dtype_ok(dtype)) return 0;
   return 4 * act_bwd_part_floats(M, N);
@@ -138,8 +152,8 @@ INSTANT_API instant_status instant_linear_bwd(const void* gz, const void* w, con
   if (M > 0 && (!gz || (gx && !w) || (gw && !x && !xq))) return INSTANT_E_ARG;
   const bool bf = dtype == INSTANT_BF16;
   TRY(workspace_ok(workspace, workspace_bytes,
-                   std::max(gx ? 4 * linear_part_floats(bf, Prod::Gx, M, N, K, false) : 0,
-                            gw ? 4 * linear_part_floats(bf, Prod::Gw, M, N, K, xq != nullptr) : 0)));
+                   std::max(gx ? linear_gx_bytes(bf, M, N, K) : 0,
+                            gw ? linear_gw_bytes(bf, M, N, K, xq != nullptr) : 0)));
   hipError_t e = hipSuccess;
   if (gx && M > 0) e = launch_linear_gx(bf, gz, w, M, N, K, gx, (float*)workspace, S(stream));
   if (e == hipSuccess && gw)

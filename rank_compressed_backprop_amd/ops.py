@@ -31,6 +31,8 @@ _sig = {
     "instant_linear_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "instant_linear_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "instant_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "instant_linear_gx_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_linear_gw_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "instant_act_bwd_workspace_bytes": (_sz, [_i, _i, _i]),
     "instant_linear_fwd": (_st, [_vp] * 4 + [_i] * 5 + [_vp] * 5 + [_sz, _vp]),
     "instant_act_bwd": (_st, [_vp] * 4 + [_i] * 4 + [_vp] * 3 + [_sz, _vp]),
@@ -67,6 +69,14 @@ def instant_linear_fwd_workspace_bytes(M, N, K, dtype) -> int:
 
 def instant_linear_bwd_workspace_bytes(M, N, K, dtype, x_ckpt) -> int:
     return int(_lib.instant_linear_bwd_workspace_bytes(M, N, K, dtype, int(x_ckpt)))
+
+
+def instant_linear_gx_workspace_bytes(M, N, K, dtype) -> int:
+    return int(_lib.instant_linear_gx_workspace_bytes(M, N, K, dtype))
+
+
+def instant_linear_gw_workspace_bytes(M, N, K, dtype, x_ckpt) -> int:
+    return int(_lib.instant_linear_gw_workspace_bytes(M, N, K, dtype, int(x_ckpt)))
 
 
 def instant_act_bwd_workspace_bytes(M, N, dtype) -> int:
@@ -153,7 +163,8 @@ def _like(t, shape, dtype, device, name):
 
 # Sizes depend on the shapes alone.
 _fwd_bytes = functools.lru_cache(4096)(instant_linear_fwd_workspace_bytes)
-_bwd_bytes = functools.lru_cache(4096)(instant_linear_bwd_workspace_bytes)
+_gx_bytes = functools.lru_cache(4096)(instant_linear_gx_workspace_bytes)
+_gw_bytes = functools.lru_cache(4096)(instant_linear_gw_workspace_bytes)
 _act_bytes = functools.lru_cache(4096)(instant_act_bwd_workspace_bytes)
 _norm_bytes = functools.lru_cache(4096)(instant_rmsnorm_workspace_bytes)
 
@@ -333,7 +344,7 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
     elif need_gw:
         _like(x, shape, gz.dtype, dev, "x")
         xp = x.data_ptr()
-    n = _bwd_bytes(M, N, K, dt, q is not None)
+    n = max(_gx_bytes(M, N, K, dt) if need_gx else 0, _gw_bytes(M, N, K, dt, q is not None) if need_gw else 0)
     ws, wp = _workspace(n, gz)
     gx = gz.new_empty(shape) if need_gx else None
     gw = torch.empty_like(w) if need_gw else None

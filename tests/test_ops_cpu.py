@@ -198,3 +198,43 @@ def test_layers_refuse_second_derivatives(monkeypatch):
         for loss in (call().square().sum(), call().sum()):  # the incoming gradient with and without a graph
             with pytest.raises(RuntimeError, match="differentiated again"):
                 torch.autograd.grad(loss, leaves, create_graph=True)
+
+
+def test_linear_backward_asks_for_the_workspace_of_its_gradients(monkeypatch):
+    """Only the gradients that are asked for take workspace: without the weight's, the values of a
+    checkpoint are not unpacked and need no room. (What a call passes is enough, and a byte less is
+    not: the library refuses it.)"""
+    calls = []
+
+    def record(gz, w, x, xq, xs, M, N, K, dt, gx, gw, ws, n, stream):
+        calls.append((gx is not None, gw is not None, xq is not None, n))
+        assert (ws is None) == (n == 0)
+        return OK
+    sizes, real = [(8192, 16, 8), (512, 256, 1024), (2048, 64, 4096), (4, 4096, 64)], ops._lib
+
+    class Lib:
+        instant_linear_bwd = staticmethod(record)
+
+        def __getattr__(self, name):
+            return getattr(real, name)
+    monkeypatch.setattr(ops, "_lib", Lib())
+    monkeypatch.setattr(ops, "_on_device", lambda t, name: None)
+    monkeypatch.setattr(ops, "_current", lambda dev: None)
+    for M, N, K in sizes:
+        for dtype, code in ((torch.bfloat16, BF), (torch.float32, FP)):
+            gz, w, x = (torch.zeros(s, dtype=dtype) for s in ((M, N), (N, K), (M, K)))
+            x8 = ops.Checkpoint8(torch.zeros(M, K, dtype=torch.int8), torch.zeros(M, -(-K // 32), dtype=torch.uint8))
+            for xx in (x, x8):
+                for gx, gw in ((True, True), (True, False), (False, True)):
+                    del calls[:]
+                    ops.linear_backward(gz, w, xx, gx, gw)
+                    ((has_gx, has_gw, ckpt, n),) = calls
+                    assert (has_gx, has_gw) == (gx, gw)
+                    need = [ops.instant_linear_gx_workspace_bytes(M, N, K, code)] if gx else []
+                    need += [ops.instant_linear_gw_workspace_bytes(M, N, K, code, ckpt)] if gw else []
+                    assert n == max(need)
+                    assert n <= ops.instant_linear_bwd_workspace_bytes(M, N, K, code, ckpt)
+                    if n:  # (a workspace a byte smaller is refused before anything is enqueued)
+                        xs = (None, A, A) if ckpt else (A, None, None)
+                        a = (A, A, *xs, M, N, K, code, A if gx else None, A if gw else None, W, n - 1, None)
+                        assert real.instant_linear_bwd(*a) == E_SHAPE, (M, N, K, dtype, ckpt, gx, gw, n)
