@@ -199,10 +199,12 @@ class InstantLinear(torch.nn.Module):
                 return _FusedLinearFn.apply(x, self.weight, self.bias, residual, *(x8 or (None, None)), self, "exact")
             return ops.linear_forward(x, self.weight, self.bias, residual, self.activation)[0]
         mode = self.mode_of_step(self.step)
-        self.step += 1
         if plain:
-            return _InstantLinearFn.apply(x, self.weight, self, mode)
-        return _FusedLinearFn.apply(x, self.weight, self.bias, residual, *(x8 or (None, None)), self, mode)
+            y = _InstantLinearFn.apply(x, self.weight, self, mode)
+        else:
+            y = _FusedLinearFn.apply(x, self.weight, self.bias, residual, *(x8 or (None, None)), self, mode)
+        self.step += 1  # (a call that was refused is no step)
+        return y
 
     def status(self) -> str:
         return instant_status_str(self.last_status)

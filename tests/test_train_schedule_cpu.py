@@ -22,3 +22,33 @@ def test_window_schedule():
 
 def test_no_projections_yet_means_exact_backward():
     assert _modes(5, 2, 0, 5) == ["calibrate", "finalize", "exact", "exact", "exact"]
+
+
+def _bare_layer(**kw):
+    """An InstantLinear without its library handle and its device."""
+    from rank_compressed_backprop_amd.linear import InstantLinear
+    mod = InstantLinear.__new__(InstantLinear)
+    torch.nn.Module.__init__(mod)
+    mod.L, mod.Cx, mod.Cy, mod.B_max, mod.N_t, mod.N_cal, mod.step, mod.generation = 4, 8, 8, 2, 5, 2, 0, 0
+    mod.torch_dtype, mod.activation, mod.checkpoint, mod.bias = torch.float32, "none", None, None
+    mod.weight = torch.nn.Parameter(torch.zeros(8, 8))
+    for k, v in kw.items():
+        setattr(mod, k, v)
+    return mod
+
+
+@pytest.mark.parametrize("plain", [False, True])
+def test_a_refused_call_is_no_step_of_the_schedule(plain):
+    """A call whose arguments are refused ran nothing: the next one has its place in the window
+    (the step that finalizes among them)."""
+    mod = _bare_layer() if plain else _bare_layer(activation="gelu")
+    mod.step = 1
+    x = torch.zeros(2, 4, 8)
+    if plain:
+        mod.weight = torch.nn.Parameter(torch.zeros(8, 8, dtype=torch.float64))  # (not the input's type)
+        with pytest.raises(RuntimeError):
+            mod(x)
+    else:
+        with pytest.raises(ValueError):
+            mod(x, residual=torch.zeros(2, 4, 16))  # (as are tensors on the CPU)
+    assert mod.step == 1 and mod.mode_of_step(mod.step) == "finalize"
