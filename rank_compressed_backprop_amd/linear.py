@@ -185,8 +185,12 @@ class InstantLinear(torch.nn.Module):
             raise ValueError(f"x must be [B <= {self.B_max}, {self.L}, {self.Cx}], got {tuple(x.shape)}")
         if x.dtype != self.torch_dtype:
             raise TypeError(f"x must be {self.torch_dtype}")
-        if x8 is not None and (self.checkpoint != "int8" or x8.q.shape != x.shape):
-            raise ValueError("x8 is x in 8 bits, for a layer with checkpoint='int8'")
+        if x8 is not None:
+            if not isinstance(x8, ops.Checkpoint8):
+                raise TypeError(f"x8 must be a Checkpoint8, got {type(x8).__name__}")
+            if self.checkpoint != "int8":
+                raise ValueError("x8 is x in 8 bits, for a layer with checkpoint='int8'")
+            ops.check_checkpoint(x8, x.shape, x.get_device(), "x8")
         x = x.contiguous()
         plain = self.bias is None and self.activation == "none" and self.checkpoint is None and residual is None
         if residual is not None:

@@ -224,7 +224,8 @@ def _empty_ckpt(shape, like):
                        like.new_empty((*shape[:-1], -(-shape[-1] // CKPT_GROUP)), dtype=torch.uint8))
 
 
-def _ckpt(c, shape, device, name):
+def check_checkpoint(c, shape, device, name):
+    """Raises unless c is a checkpoint of a tensor of this shape on this device (its index)."""
     _like(c.q, shape, torch.int8, device, name + ".q")
     _like(c.scale, (*shape[:-1], -(-shape[-1] // CKPT_GROUP)), torch.uint8, device, name + ".scale")
 
@@ -248,7 +249,7 @@ def checkpoint_unpack(c: Checkpoint8, dtype=torch.bfloat16) -> torch.Tensor:
         raise ValueError(f"a checkpoint's last dimension is a positive multiple of 8, got {tuple(shape)}")
     _on_device(q, "q")
     dev = q.get_device()
-    _ckpt(c, shape, dev, "checkpoint")
+    check_checkpoint(c, shape, dev, "checkpoint")
     C = shape[-1]
     x = torch.empty_like(q, dtype=dtype)
     _ok(_lib.instant_ckpt_unpack(q.data_ptr(), c.scale.data_ptr(), q.numel() // C, C, code, x.data_ptr(),
@@ -305,7 +306,7 @@ def activation_backward(gy, z, activation="none", bias_grad=True):
         if not bias_grad:
             return gy, None
     elif isinstance(z, Checkpoint8):
-        _ckpt(z, gy.shape, dev, "z")
+        check_checkpoint(z, gy.shape, dev, "z")
         q, s = z.q.data_ptr(), z.scale.data_ptr()
     elif z is None:
         raise ValueError(f"activation {activation!r} needs z")
@@ -339,7 +340,7 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
     shape = (*gz.shape[:-1], K)
     xp = q = s = None
     if isinstance(x, Checkpoint8):
-        _ckpt(x, shape, dev, "x")
+        check_checkpoint(x, shape, dev, "x")
         q, s = x.q.data_ptr(), x.scale.data_ptr()
     elif need_gw:
         _like(x, shape, gz.dtype, dev, "x")

@@ -52,3 +52,20 @@ def test_a_refused_call_is_no_step_of_the_schedule(plain):
         with pytest.raises(ValueError):
             mod(x, residual=torch.zeros(2, 4, 16))  # (as are tensors on the CPU)
     assert mod.step == 1 and mod.mode_of_step(mod.step) == "finalize"
+
+
+def test_x8_is_checked_in_the_forward():
+    """A checkpoint that does not fit x is refused by the call it is given to, not by the backward
+    pass of a step that has run."""
+    from rank_compressed_backprop_amd import ops
+    x = torch.zeros(2, 4, 8)
+    q, s = torch.zeros(2, 4, 8, dtype=torch.int8), torch.zeros(2, 4, 1, dtype=torch.uint8)
+    for exc, x8 in [(ValueError, ops.Checkpoint8(q[:1], s)), (ValueError, ops.Checkpoint8(q, s[:1])),
+                    (TypeError, ops.Checkpoint8(q.float(), s)), (TypeError, ops.Checkpoint8(q, s.to(torch.int8))),
+                    (ValueError, ops.Checkpoint8(q.transpose(0, 1).contiguous().transpose(0, 1), s)),
+                    (TypeError, q), (TypeError, (q, s))]:
+        mod = _bare_layer(checkpoint="int8")
+        with pytest.raises(exc, match="x8"):
+            mod(x, x8=x8)
+    with pytest.raises(ValueError, match="x8"):
+        _bare_layer(activation="gelu")(x, x8=ops.Checkpoint8(q, s))
