@@ -33,7 +33,8 @@ class _RMSNormFn(torch.autograd.Function):
 
 
 class InstantRMSNorm(torch.nn.Module):
-    """RMS norm over the last dimension (C channels, a multiple of 8), weight [C] of ones.
+    """RMS norm over the last dimension (C channels, a multiple of 8), weight [C] of ones;
+    dtype is the type of the weight and of the inputs ("bf16" or "fp32").
 
     forward(x, residual=None) returns ops.NormOut's y and h: (y, h) with a residual, where
     h = x + residual is the new residual stream, else y. With checkpoint="int8" a Checkpoint8 of
@@ -44,6 +45,10 @@ class InstantRMSNorm(torch.nn.Module):
         super().__init__()
         if checkpoint not in (None, "int8"):
             raise ValueError(f"checkpoint must be None or 'int8', got {checkpoint!r}")
+        if dtype not in ("bf16", "fp32"):
+            raise ValueError(f"dtype must be 'bf16' or 'fp32', got {dtype!r}")
+        if C < 8 or C % 8:
+            raise ValueError(f"C must be a positive multiple of 8, got {C}")
         self.C, self.eps, self.checkpoint = int(C), float(eps), checkpoint
         self.weight = torch.nn.Parameter(torch.ones(self.C, device=device, dtype=torch.bfloat16 if dtype == "bf16"
                                                     else torch.float32))

@@ -17,6 +17,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch import Tensor
 
 from . import INSTANT_BF16, INSTANT_FP32, INSTANT_OK, InstantError, _lib, _ptr, _stream
 
@@ -120,7 +121,13 @@ def _ok(status, where):
         raise InstantError(status, where)
 
 
+def _foreign(t, name):
+    raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+
+
 def _dtype(t, name):
+    if not isinstance(t, Tensor):
+        _foreign(t, name)
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
@@ -151,6 +158,8 @@ def _matrix(t, name):
 
 def _like(t, shape, dtype, device, name):
     """Another tensor of the call: of this shape and type, beside the first."""
+    if not isinstance(t, Tensor):
+        _foreign(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -244,6 +253,10 @@ def checkpoint_unpack(c: Checkpoint8, dtype=torch.bfloat16) -> torch.Tensor:
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    if not isinstance(c, Checkpoint8):
+        raise TypeError(f"a checkpoint must be a Checkpoint8, got {type(c).__name__}")
+    if not isinstance(c.q, Tensor):
+        _foreign(c.q, "checkpoint.q")
     q, shape = c.q, c.q.shape
     if q.dim() < 1 or shape[-1] < 8 or shape[-1] % 8:
         raise ValueError(f"a checkpoint's last dimension is a positive multiple of 8, got {tuple(shape)}")
@@ -268,6 +281,8 @@ def linear_forward(x, w, bias=None, residual=None, activation="none", save="none
     act = _act(activation)
     if save not in ("none", "z", "z8"):
         raise ValueError(f"save must be none, z or z8, got {save!r}")
+    if not isinstance(w, Tensor):
+        _foreign(w, "w")
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
     N, dev = w.shape[0], x.get_device()
@@ -331,6 +346,8 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
     M, N, dt = _matrix(gz, "gz")
     if not (need_gx or need_gw):
         return None, None
+    if not isinstance(w, Tensor):
+        _foreign(w, "w")
     if w.dim() != 2:
         raise ValueError(f"w must be [N, K], got {tuple(w.shape)}")
     K, dev = w.shape[1], gz.get_device()
@@ -343,6 +360,8 @@ def linear_backward(gz, w, x, need_gx=True, need_gw=True):
         check_checkpoint(x, shape, dev, "x")
         q, s = x.q.data_ptr(), x.scale.data_ptr()
     elif need_gw:
+        if x is None:
+            raise ValueError("x is needed for the weight's gradient")
         _like(x, shape, gz.dtype, dev, "x")
         xp = x.data_ptr()
     n = max(_gx_bytes(M, N, K, dt) if need_gx else 0, _gw_bytes(M, N, K, dt, q is not None) if need_gw else 0)

@@ -238,3 +238,33 @@ def test_linear_backward_asks_for_the_workspace_of_its_gradients(monkeypatch):
                         xs = (None, A, A) if ckpt else (A, None, None)
                         a = (A, A, *xs, M, N, K, code, A if gx else None, A if gw else None, W, n - 1, None)
                         assert real.instant_linear_bwd(*a) == E_SHAPE, (M, N, K, dtype, ckpt, gx, gw, n)
+
+
+def test_missing_and_foreign_arguments(monkeypatch):
+    """What is needed and not given, and what is neither a tensor nor a checkpoint, is named."""
+    monkeypatch.setattr(ops, "_on_device", lambda t, name: None)
+    gz, w, x = torch.zeros(4, 16), torch.zeros(16, 8), torch.zeros(4, 8)
+    c = (torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4, 1, dtype=torch.uint8))  # a pair, no Checkpoint8
+    for exc, name, call in [(ValueError, "x", lambda: ops.linear_backward(gz, w, None)),
+                            (TypeError, "x", lambda: ops.linear_backward(gz, w, c)),
+                            (TypeError, "z", lambda: ops.activation_backward(gz, c, "relu")),
+                            (TypeError, "bias", lambda: ops.linear_forward(x, w, bias=1.0)),
+                            (TypeError, "w", lambda: ops.linear_forward(x, None)),
+                            (TypeError, "w", lambda: ops.linear_backward(gz, None, x)),
+                            (TypeError, "x", lambda: ops.checkpoint_pack(None)),
+                            (TypeError, "h", lambda: ops.rmsnorm_backward(x, None, w[0], x[:, 0])),
+                            (TypeError, "checkpoint", lambda: ops.checkpoint_unpack(c))]:
+        with pytest.raises(exc, match=f"^(a )?{name} "):
+            call()
+
+
+def test_norm_layer_refuses_other_types():
+    from rank_compressed_backprop_amd.norm import InstantRMSNorm
+    for dtype in ("float16", "bfloat16", torch.bfloat16, None):
+        with pytest.raises(ValueError, match="dtype"):
+            InstantRMSNorm(64, dtype=dtype, device="cpu")
+    assert InstantRMSNorm(64, device="cpu").weight.dtype == torch.bfloat16
+    assert InstantRMSNorm(64, dtype="fp32", device="cpu").weight.dtype == torch.float32
+    for C in (0, 12, -8):
+        with pytest.raises(ValueError, match="C must"):
+            InstantRMSNorm(C, device="cpu")
