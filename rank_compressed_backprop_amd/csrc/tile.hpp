@@ -2,16 +2,9 @@
 #pragma once
 
 #include "ops.hpp"
+#include "plan.hpp"
 
 namespace instant {
-
-// Tile (wm, wn: 16-row tiles of a wave; a block is 32 wm x 32 wn), stages held in LDS and K
-// slices of a product.
-struct Plan {
-  int wm, wn, ns, S;
-  bool part;  // float32 partials instead of the output (S > 1 needs it)
-  bool add;   // added to those that are there
-};
 
 // C(m, n) = sum_k A(m, k) B(n, k) for an M x N output (N % 8 == 0), K >= 1:
 //   fwd: A [M][lda], B [N][ldb], K % 8 == 0     gx: A [M][lda], B [K][ldb], K % 8 == 0

@@ -278,6 +278,38 @@ def test_every_tile(which):
                 within("gw", gw, ref, u * ref.abs() + (1 + u) * GAMMA(M) * mag + 1e-38)
 
 
+# The largest tile with the contraction split, which the forward's lists above do not reach.
+LARGEST_SPLIT = {BF: [(3629, 1040, 4976)], FP: [(4128, 1224, 3144)]}
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_linear_forward_largest_tile_split(dtype):
+    from rank_compressed_backprop_amd import ops
+    for a, b, k in LARGEST_SPLIT[dtype]:
+        check_forward(ops, a, b, k, dtype, "none", True, True, "z")
+        check_forward(ops, a, b, k, dtype, "none", False, False, "none")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_residual_in_place_in_every_tile(dtype):
+    """The residual may be the output itself: the same bits as beside it, in every tile."""
+    import rank_compressed_backprop_amd as rcb
+    from rank_compressed_backprop_amd import ops
+    code = rcb.INSTANT_BF16 if dtype == BF else rcb.INSTANT_FP32
+    for M, N, K in EVERY_TILE["fwd", dtype] + LARGEST_SPLIT[dtype]:
+        g = gen("in place", M, N, K)
+        x, w = randn(g, M, K, dtype=dtype), randn(g, N, K, dtype=dtype, sd=K ** -0.5)
+        b, r = randn(g, N, dtype=dtype), randn(g, M, N, dtype=dtype)
+        n = ops.instant_linear_fwd_workspace_bytes(M, N, K, code)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+        for act in ("none", "silu"):  # (two choices of tiles)
+            print(f"[in place] {M} {N} {K} {dtype} {act}", flush=True)
+            want, _ = ops.linear_forward(x, w, b, r, act)
+            y = r.clone()
+            assert ops.instant_linear_fwd(x, w, b, y, M, N, K, code, ops.ACTIVATIONS[act], y, None, None, None, ws, n) == 0
+            assert torch.equal(bits(y), bits(want))
+
+
 def test_linear_forward_nonfinite_stays():
     """An infinity or NaN in one row reaches that row's outputs, and no other row's."""
     from rank_compressed_backprop_amd import ops
@@ -292,6 +324,47 @@ def test_linear_forward_nonfinite_stays():
                 assert bool(torch.isnan(y[1]).all()) and bool(torch.isnan(value64(z)[1]).all())
                 keep = torch.arange(M) != 1
                 assert torch.equal(bits(y[keep]), bits(clean[keep]))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_forward_extreme_values(act, dtype):
+    """Infinities, NaN and numbers near the type's end in one row of x, of the residual and of the
+    bias: infinite and NaN outputs where the definition in 64 bits has them (an infinity below zero
+    times a vanished factor is NaN there too), right values elsewhere, other rows as ever."""
+    from rank_compressed_backprop_amd import ops
+    u = U[dtype]
+    for M, N, K in [(3, 72, 64), (200, 264, 320)]:
+        g = gen("extreme", M, act)
+        x, w = randn(g, M, K, dtype=dtype), randn(g, N, K, dtype=dtype)
+        b, r = randn(g, N, dtype=dtype), randn(g, M, N, dtype=dtype)
+        clean, _ = ops.linear_forward(x, w, b, r, act)
+        keep = torch.arange(M) != 1
+        for value in (float("nan"), float("inf"), -float("inf"), 3e19, -3e19, 2e37, -2e37):
+            for place in ("x", "r", "b"):
+                print(f"[extreme] {M} {N} {K} {dtype} {act} {value} in {place}", flush=True)
+                t = {"x": x.clone(), "r": r.clone(), "b": b.clone()}
+                if place == "b":
+                    t["b"][N - 3] = value
+                else:
+                    t[place][1, 5] = value  # (x: a term of every column's sum)
+                y, z = ops.linear_forward(t["x"], w, t["b"], t["r"], act, save="z")
+                z64 = t["x"].double() @ w.double().t() + t["b"].double()
+                y64 = act64(z64, act) + t["r"].double()
+                for got, ref in ((z, z64), (y, y64)):
+                    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+                    assert torch.equal(torch.isposinf(got), torch.isposinf(ref))
+                    assert torch.equal(torch.isneginf(got), torch.isneginf(ref))
+                mag = t["x"].double().abs() @ w.double().abs().t() + t["b"].double().abs()
+                ez = GAMMA(K) * mag
+                ey = 1.13 * ez + 2.0 ** -19 * z64.abs().clamp(min=1) + 2.0 ** -23 * (y64.abs() + t["r"].double().abs())
+                fine = torch.isfinite(y64) & torch.isfinite(mag)
+                within("y", y[fine], y64[fine], (u * y64.abs() + (1 + u) * ey + 1e-38)[fine])
+                if place == "b":
+                    other = torch.arange(N) != N - 3
+                    assert torch.equal(bits(y[:, other]), bits(clean[:, other]))
+                else:
+                    assert torch.equal(bits(y[keep]), bits(clean[keep]))
 
 
 # ------------------------------------------------------------------------- linear, backward
