@@ -4,8 +4,9 @@
 //   gx = rstd (u - h rstd^2 mean(u h)) + gh, u = gy g;  gg = sum_m gy h rstd
 //
 // Both are one pass over memory: a row stays in its threads' registers between its statistic
-// and its outputs. A row of up to 2048 channels belongs to one wave (no barrier), a longer one
-// to a block. The checkpoint is taken from the rounded y, so it is what packing y would give.
+// and its outputs (the gradients' rows of more than 16384 channels are read a second time: with
+// their sums and two operands they do not fit). A row of up to 2048 channels belongs to one wave
+// (no barrier), a longer one to a block. The checkpoint is taken from the rounded y, so it is what packing y would give.
 #include <algorithm>
 
 #include "ops.hpp"

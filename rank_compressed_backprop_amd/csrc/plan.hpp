@@ -24,7 +24,8 @@ namespace planning {
 // The figures are fitted to measured times on gfx950 of 69 products in bfloat16 (three layouts, 1
 // to 16384 rows, columns and k) and 51 in float32, by 9 tile shapes and ring depths by 8 splits.
 // The choice is within 5% of the best of all measured in 66 of the 69 (1.4% behind on average)
-// and 44 of the 51 (3%). What the choice is worth in bfloat16, best against a fixed 256 x 256
+// and in 42 of the 50 whose choice was measured (3.4%; 20 x 3000 over 1000 is 15.7 against 10.3 us).
+// What the choice is worth in bfloat16, best against a fixed 256 x 256
 // tile: 8 x 11008 over 4096 15.0 against 73 us, 768 x 768 over 16384 40 against 309 us, 512 x 4096
 // over 1024 8.5 against 31 us; against a fixed 64 x 64 tile: 16384 x 1024 over 4096 108 against
 // 197 us. In float32 the matrix cores have an eighth of the rate, nothing else holds them up, and
@@ -34,7 +35,11 @@ namespace planning {
 // tiles that have a compute unit to themselves more: nothing runs beside it. (bfloat16 with
 // GELU and an 8-bit pre-activation, 256 x 192 against 128 x 128 tiles: 16384 x 768 over 768 35.5
 // against 33.0 us, without them 26.3 against 27.7; 6272 x 1792 over 448 29.9 against 25.3 us; but
-// 16384 x 11008 over 4096, whose stages outweigh it, 1196 with 256 x 256 against 1512 us.)
+// 16384 x 11008 over 4096, whose stages outweigh it, 1212 with 256 x 256 against 1515 us.) The two
+// factors are shared by all shapes, and the 128 x 128 tile with two blocks a unit costs more over
+// long contractions than the rule says: M x 11008 over 4096 with GELU and an 8-bit pre-activation
+// takes 128 x 128 for M = 4096, 8192, 12288 and 14336 (349, 769, 1138 and 1232 us) where 256 x 256
+// is faster (331, 651, 964 and 1087).
 struct Shape {
   int wm, wn, ns, fit;
   float lone, each, ends;
