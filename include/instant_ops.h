@@ -3,7 +3,10 @@
  * its forward with bias, activation and residual, its exact backward from activations kept
  * in 8 bits, and the RMS norm that produces its input. They are stateless (no handle): the
  * low-rank path of instant.h compresses what a layer keeps between calibrations, these serve
- * the steps whose backward is exact, and the parts of a layer around the product.
+ * the steps whose backward is exact, and the parts of a layer around the product. Behind them
+ * stand the operators at a language model's two ends, tokens to rows and logits to log
+ * probabilities, with their gradients, and a step's last act before the optimizer: the norm over
+ * all gradients, and clipping.
  *
  * Shapes and layouts (all row-major, contiguous, M = rows = tokens of all samples):
  *   x     [M, K]    the layer's input            w    [N, K]   weight (y = x . w^T)
@@ -129,6 +132,73 @@ size_t instant_rmsnorm_workspace_bytes(int32_t M, int32_t C);
 instant_status instant_rmsnorm_bwd(const void* gy, const void* h, const void* g, const float* rstd, const void* gh,
                                    int32_t M, int32_t C, int32_t dtype, void* gx, void* gg, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/* ---- The ends of a training step. Differences from the conventions above:
+ *   - Tokens and targets are integers of token_bytes bytes (4 or 8), aligned to their size.
+ *   - A vocabulary is 1 <= V <= 2^18; logits have rows of any width, so V need not be a multiple
+ *     of 8, and they and their gradient are aligned to an element only.
+ *   - What integers hold is not known on the host. One outside 0 .. V - 1 (and not the ignored or
+ *     padding one) reads nothing out of range: its row of y, its log probability and its row of gz
+ *     are NaN, so the fault is not hidden; the table's gradient has no place for it. */
+
+/* y = scale * table[tokens] [M, C], for table [V, C] (rounded once; exact for scale 1). */
+instant_status instant_embed_fwd(const void* tokens, int32_t token_bytes, int32_t M, const void* table, int32_t V,
+                                 int32_t C, int32_t dtype, float scale, void* y, void* stream);
+
+/* Bytes of workspace for instant_embed_bwd (0: nothing, or sizes that are not accepted). */
+size_t instant_embed_workspace_bytes(int32_t M, int32_t V, int32_t C);
+
+/* The table's gradient: gtable[v] = scale * sum of the rows of gy [M, C] whose token is v, added in
+ * float32 in the order of the rows; rows without a token are zeros. Rows whose token is `padding`
+ * (-1: none) take no part. accumulate != 0: the sums are added to what gtable holds (and rounded
+ * once), rows without a token stay as they are. M <= 2^22, M * C <= 2^36. */
+instant_status instant_embed_bwd(const void* gy, const void* tokens, int32_t token_bytes, int32_t M, int32_t V,
+                                 int32_t C, int32_t dtype, float scale, int64_t padding, int32_t accumulate,
+                                 void* gtable, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Log probabilities from logits [M, W], of whose columns the first V <= W <= 2^18 count. Each of
+ *   logp     float [M]     log of the probability of targets[m]; 0 where that is `ignore`
+ *   lse      float [M]     log sum exp(logits)
+ *   entropy  float [M]     -sum p log p
+ *   stats    float [M, 2]  the largest logit and the log of sum exp(logits - it), for the gradient
+ *   top_logp float [M, k], top_index int64 [M, k]   the k <= 32, k <= V likeliest in order, equal
+ *                          ones by their place (-0 is 0), and their log probabilities
+ * may be NULL; targets may be NULL with logp (and must be given with it), and both top_* are given
+ * exactly when k > 0.
+ * A logit of -inf has probability 0 (log probability -inf). A row of nothing else has probability 0
+ * throughout: lse -inf, entropy 0, log probabilities -inf, alternatives 0 .. k - 1. A NaN or +inf
+ * makes its row's results NaN; among the alternatives a NaN ranks with -inf. */
+instant_status instant_logprobs_fwd(const void* logits, const void* targets, int32_t token_bytes, int32_t M,
+                                    int32_t W, int32_t V, int32_t dtype, int64_t ignore, int32_t k, float* logp,
+                                    float* lse, float* entropy, float* stats, float* top_logp, int64_t* top_index,
+                                    void* stream);
+
+/* The logits' gradient gz [M, W] for gradients g_logp, g_lse, g_entropy [M] (each may be NULL, not
+ * all) of logp, lse and entropy, with stats and (for g_entropy) entropy from the forward pass:
+ *   gz_j = g_logp (1[j = t] - p_j) + g_lse p_j - g_entropy p_j (log p_j + entropy),   j < V
+ * and 0 in the columns behind V. g_logp needs targets, and takes no part where they are `ignore`.
+ * A row whose gradients are all 0 gets zeros, whatever it holds. gz may be logits itself. */
+instant_status instant_logprobs_bwd(const void* logits, const void* targets, int32_t token_bytes, int32_t M,
+                                    int32_t W, int32_t V, int32_t dtype, int64_t ignore, const float* stats,
+                                    const float* entropy, const float* g_logp, const float* g_lse,
+                                    const float* g_entropy, void* gz, void* stream);
+
+/* The Euclidean norm over n tensors, norm[0] = (sum of all squares)^(1/2) float32, summed in
+ * float64. grads, count and dtype are host arrays, read before the call returns: device pointers
+ * (aligned to an element; NULL where count is 0), elements (0 <= count <= 2^40) and instant_dtype.
+ * 0 <= n <= 2^20. A tensor that is listed twice counts twice. */
+size_t instant_grad_norm_workspace_bytes(int32_t n);
+instant_status instant_grad_norm(const void* const* grads, const int64_t* count, const int32_t* dtype, int32_t n,
+                                 float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same norm, and out[i] = c * grads[i] with c = 1 if norm + 1e-6 <= max_norm, else
+ * max_norm / (norm + 1e-6) (max_norm >= 0, infinity allowed). Each product is rounded once to
+ * out_dtype[i]. out[i] may be grads[i] itself in the same type; no other overlap of an output with
+ * an output or a gradient is accepted (E_ARG). A NaN norm makes everything NaN, an infinite one
+ * gives c = 0 (unless max_norm is infinite). */
+instant_status instant_clip_grads(const void* const* grads, const int64_t* count, const int32_t* dtype,
+                                  void* const* out, const int32_t* out_dtype, int32_t n, float max_norm, float* norm,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,7 +21,8 @@ OBJDIR = os.path.join(REPO, "_build")
 SOURCES = ["kernels_proj.hip", "kernels_hot.hip", "kernels_gemm.hip", "kernels_calib.hip", "kernels_eig.hip",
            "kernels_linear.hip", "kernels_tile_bf16_fwd.hip", "kernels_tile_bf16_gx.hip", "kernels_tile_bf16_gw.hip",
            "kernels_tile_fp32_fwd.hip", "kernels_tile_fp32_gx.hip", "kernels_tile_fp32_gw.hip",
-           "kernels_ckpt.hip", "kernels_norm.hip", "instant_api.cpp", "ops_api.cpp"]
+           "kernels_ckpt.hip", "kernels_norm.hip", "kernels_embed.hip", "kernels_logprobs.hip",
+           "kernels_clip.hip", "instant_api.cpp", "ops_api.cpp"]
 
 COMMON = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-fvisibility=hidden",
           "-I" + INCLUDE, "-I" + CSRC]

@@ -1,5 +1,6 @@
-// Shared by the operators around the linear layer (include/instant_ops.h): the 8-bit
-// checkpoint format, activations and their slopes, the GEMM epilogue, host launchers.
+// Shared by the operators around the linear layer and at a training step's ends
+// (include/instant_ops.h): the 8-bit checkpoint format, activations and their slopes, the GEMM
+// epilogue, host launchers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +10,7 @@
 #include <utility>
 
 #include "common.hpp"
+#include "launch.hpp"
 
 namespace instant {
 
@@ -307,5 +309,31 @@ hipError_t launch_rmsnorm_fwd(bool bf16_io, const void* x, const void* res, cons
 size_t rmsnorm_part_floats(int M, int C);
 hipError_t launch_rmsnorm_bwd(bool bf16_io, const void* gy, const void* h, const void* g, const float* rstd,
                               const void* gh, int M, int C, void* gx, void* gg, float* part, hipStream_t st);
+
+// Tokens are int64 (wide) or int32.
+hipError_t launch_embed_fwd(bool bf16_io, const void* tokens, bool wide, int M, const void* w, int V, int C,
+                            float scale, void* y, hipStream_t st);
+constexpr int EMBED_MAX_M = 1 << 22;  // tokens of a gradient
+size_t embed_bwd_bytes(int M, int C);
+// gw [V][C]: overwritten, or (add) the sums are added to it.
+hipError_t launch_embed_bwd(bool bf16_io, const void* gy, const void* tokens, bool wide, int M, int V, int C,
+                            float scale, int64_t padding, bool add, void* gw, void* ws, hipStream_t st);
+
+constexpr int LOGPROBS_MAX_TOP = 32;
+// Logits [M][W], of which the first V columns count; outputs that are null are not written.
+hipError_t launch_logprobs_fwd(bool bf16_io, const void* z, const void* targets, bool wide, int M, int W, int V,
+                               int64_t ignore, int k, float* logp, float* lse, float* entropy, float* stats,
+                               float* top_logp, int64_t* top_index, hipStream_t st);
+hipError_t launch_logprobs_bwd(bool bf16_io, const void* z, const void* targets, bool wide, int M, int W, int V,
+                               int64_t ignore, const float* stats, const float* entropy, const float* g_logp,
+                               const float* g_lse, const float* g_ent, void* gz, hipStream_t st);
+
+// n tensors of count[i] elements, bf[i]: bfloat16, else float32 (all host arrays). factor: the
+// clipping factor is left at ws.
+size_t grad_norm_bytes(int n);
+hipError_t launch_grad_norm(const void* const* src, const int64_t* count, const int32_t* bf, int n, float max_norm,
+                            float* norm, void* ws, hipStream_t st, bool factor);
+hipError_t launch_clip_grads(const void* const* src, const int64_t* count, const int32_t* bf, void* const* dst,
+                             const int32_t* dst_bf, int n, float max_norm, float* norm, void* ws, hipStream_t st);
 
 }  // namespace instant

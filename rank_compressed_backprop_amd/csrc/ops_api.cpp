@@ -1,9 +1,11 @@
-// C entry points of the operators around the linear layer (include/instant_ops.h): argument
-// checks and workspace use; every step is a stream-ordered launch.
+// C entry points of the operators around the linear layer and at a training step's ends
+// (include/instant_ops.h): argument checks and workspace use; every step is a stream-ordered launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <new>
+#include <vector>
 
 #include "instant_ops.h"
 #include "ops.hpp"
@@ -192,4 +194,164 @@ INSTANT_API instant_status instant_rmsnorm_bwd(const void* gy, const void* h, co
   TRY(workspace_ok(workspace, workspace_bytes, gg ? 4 * rmsnorm_part_floats(M, C) : 0));
   return hip_ok(launch_rmsnorm_bwd(dtype == INSTANT_BF16, gy, h, g, rstd, gh, M, C, gx, gg, (float*)workspace,
                                    S(stream)));
+}
+
+namespace {
+
+bool tokens_ok(const void* t, int32_t bytes) { return (bytes == 4 || bytes == 8) && ((uintptr_t)t) % bytes == 0; }
+
+// 1 <= V <= W <= MAX_WIDTH, of any residue
+instant_status vocab(int32_t M, int32_t W, int32_t V) {
+  if (M < 0 || V < 1 || W < V) return INSTANT_E_ARG;
+  return M > MAX_ROWS || W > MAX_WIDTH ? INSTANT_E_SHAPE : INSTANT_OK;
+}
+
+// logits may start at any element, as rows cut out of a matrix of odd width do
+bool logits_ok(const void* z, int32_t dtype) { return ((uintptr_t)z) % (dtype == INSTANT_BF16 ? 2 : 4) == 0; }
+
+template <class... P> bool off4(P... p) { return (... || (((uintptr_t)p) % 4)); }
+
+instant_status embed_sizes(int32_t M, int32_t V, int32_t C) {
+  TRY(sizes(M, {C}));
+  if (V < 1) return INSTANT_E_ARG;
+  return V > MAX_WIDTH ? INSTANT_E_SHAPE : INSTANT_OK;
+}
+
+instant_status embed_bwd_sizes(int32_t M, int32_t V, int32_t C) {
+  TRY(embed_sizes(M, V, C));
+  return M > EMBED_MAX_M || (int64_t)M * C > (int64_t)1 << 36 ? INSTANT_E_SHAPE : INSTANT_OK;
+}
+
+constexpr int32_t MAX_TENSORS = 1 << 20;
+
+instant_status tensors(const void* const* p, const int64_t* count, const int32_t* dtype, int32_t n) {
+  if (n < 0 || (n > 0 && (!p || !count || !dtype))) return INSTANT_E_ARG;
+  if (n > MAX_TENSORS) return INSTANT_E_SHAPE;
+  for (int32_t i = 0; i < n; ++i) {
+    if (count[i] < 0 || !dtype_ok(dtype[i])) return INSTANT_E_ARG;
+    if (count[i] > (int64_t)1 << 40) return INSTANT_E_SHAPE;
+    if (count[i] && (!p[i] || ((uintptr_t)p[i]) % (dtype[i] == INSTANT_BF16 ? 2 : 4))) return INSTANT_E_ARG;
+  }
+  return INSTANT_OK;
+}
+
+// Whether an output of clip_grads shares memory with another tensor of the call (other than an
+// output with its own gradient, of the same type in the same place). Two intervals that overlap
+// are found by a sweep over the starts; gradients may share memory with each other.
+bool outputs_overlap(const void* const* g, void* const* out, const int64_t* count, const int32_t* dtype,
+                     const int32_t* out_dtype, int32_t n) {
+  struct Span {
+    uintptr_t a, b;
+    bool out;
+  };
+  std::vector<Span> v;
+  v.reserve(2 * (size_t)n);
+  for (int32_t i = 0; i < n; ++i) {
+    if (!count[i]) continue;
+    const uintptr_t a = (uintptr_t)g[i], o = (uintptr_t)out[i];
+    v.push_back({o, o + (uintptr_t)count[i] * (out_dtype[i] == INSTANT_BF16 ? 2 : 4), true});
+    if (a != o || dtype[i] != out_dtype[i])
+      v.push_back({a, a + (uintptr_t)count[i] * (dtype[i] == INSTANT_BF16 ? 2 : 4), false});
+  }
+  std::sort(v.begin(), v.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
+  uintptr_t any = 0, outs = 0;  // the furthest ends so far
+  for (const Span& s : v) {
+    if (s.a < (s.out ? any : outs)) return true;
+    any = std::max(any, s.b);
+    if (s.out) outs = std::max(outs, s.b);
+  }
+  return false;
+}
+
+}  // namespace
+
+INSTANT_API instant_status instant_embed_fwd(const void* tokens, int32_t token_bytes, int32_t M, const void* table,
+                                             int32_t V, int32_t C, int32_t dtype, float scale, void* y, void* stream) {
+  TRY(embed_sizes(M, V, C));
+  if (!dtype_ok(dtype) || !tokens_ok(tokens, token_bytes) || off16(table, y) || !std::isfinite(scale))
+    return INSTANT_E_ARG;
+  if (M == 0) return INSTANT_OK;
+  if (!tokens || !table || !y) return INSTANT_E_ARG;
+  return hip_ok(
+      launch_embed_fwd(dtype == INSTANT_BF16, tokens, token_bytes == 8, M, table, V, C, scale, y, S(stream)));
+}
+
+INSTANT_API size_t instant_embed_workspace_bytes(int32_t M, int32_t V, int32_t C) {
+  if (embed_bwd_sizes(M, V, C) != INSTANT_OK) return 0;
+  return embed_bwd_bytes(M, C);
+}
+
+INSTANT_API instant_status instant_embed_bwd(const void* gy, const void* tokens, int32_t token_bytes, int32_t M,
+                                             int32_t V, int32_t C, int32_t dtype, float scale, int64_t padding,
+                                             int32_t accumulate, void* gtable, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  TRY(embed_bwd_sizes(M, V, C));
+  if (!dtype_ok(dtype) || !tokens_ok(tokens, token_bytes) || off16(gy, gtable) || !std::isfinite(scale) || !gtable ||
+      padding < -1)
+    return INSTANT_E_ARG;
+  if (M > 0 && (!gy || !tokens)) return INSTANT_E_ARG;
+  TRY(workspace_ok(workspace, workspace_bytes, embed_bwd_bytes(M, C)));
+  return hip_ok(launch_embed_bwd(dtype == INSTANT_BF16, gy, tokens, token_bytes == 8, M, V, C, scale, padding,
+                                 accumulate != 0, gtable, workspace, S(stream)));
+}
+
+INSTANT_API instant_status instant_logprobs_fwd(const void* logits, const void* targets, int32_t token_bytes,
+                                                int32_t M, int32_t W, int32_t V, int32_t dtype, int64_t ignore,
+                                                int32_t k, float* logp, float* lse, float* entropy, float* stats,
+                                                float* top_logp, int64_t* top_index, void* stream) {
+  TRY(vocab(M, W, V));
+  if (!dtype_ok(dtype) || !tokens_ok(targets, token_bytes) || !logits_ok(logits, dtype) ||
+      off4(logp, lse, entropy, stats, top_logp) || ((uintptr_t)top_index) % 8)
+    return INSTANT_E_ARG;
+  if (k < 0) return INSTANT_E_ARG;
+  if (k > LOGPROBS_MAX_TOP || k > V) return INSTANT_E_SHAPE;
+  if (M == 0) return INSTANT_OK;
+  if (!logits || (targets == nullptr) != (logp == nullptr)) return INSTANT_E_ARG;
+  if ((k > 0) != (top_logp != nullptr) || (k > 0) != (top_index != nullptr)) return INSTANT_E_ARG;
+  if (!logp && !lse && !entropy && !stats && !k) return INSTANT_E_ARG;
+  return hip_ok(launch_logprobs_fwd(dtype == INSTANT_BF16, logits, targets, token_bytes == 8, M, W, V, ignore, k, logp,
+                                    lse, entropy, stats, top_logp, top_index, S(stream)));
+}
+
+INSTANT_API instant_status instant_logprobs_bwd(const void* logits, const void* targets, int32_t token_bytes,
+                                                int32_t M, int32_t W, int32_t V, int32_t dtype, int64_t ignore,
+                                                const float* stats, const float* entropy, const float* g_logp,
+                                                const float* g_lse, const float* g_entropy, void* gz, void* stream) {
+  TRY(vocab(M, W, V));
+  if (!dtype_ok(dtype) || !tokens_ok(targets, token_bytes) || !logits_ok(logits, dtype) || !logits_ok(gz, dtype) ||
+      off4(stats, entropy, g_logp, g_lse, g_entropy))
+    return INSTANT_E_ARG;
+  if (M == 0) return INSTANT_OK;
+  if (!logits || !stats || !gz || (!g_logp && !g_lse && !g_entropy)) return INSTANT_E_ARG;
+  if ((g_logp && !targets) || (g_entropy && !entropy)) return INSTANT_E_ARG;
+  return hip_ok(launch_logprobs_bwd(dtype == INSTANT_BF16, logits, targets, token_bytes == 8, M, W, V, ignore, stats,
+                                    entropy, g_logp, g_lse, g_entropy, gz, S(stream)));
+}
+
+INSTANT_API size_t instant_grad_norm_workspace_bytes(int32_t n) {
+  return n < 0 || n > MAX_TENSORS ? 0 : grad_norm_bytes(n);
+}
+
+INSTANT_API instant_status instant_grad_norm(const void* const* grads, const int64_t* count, const int32_t* dtype,
+                                             int32_t n, float* norm, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  TRY(tensors(grads, count, dtype, n));
+  if (!norm || off4(norm)) return INSTANT_E_ARG;
+  TRY(workspace_ok(workspace, workspace_bytes, grad_norm_bytes(n)));
+  return hip_ok(launch_grad_norm(grads, count, dtype, n, 0.0f, norm, workspace, S(stream), false));
+}
+
+INSTANT_API instant_status instant_clip_grads(const void* const* grads, const int64_t* count, const int32_t* dtype,
+                                              void* const* out, const int32_t* out_dtype, int32_t n, float max_norm,
+                                              float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  TRY(tensors(grads, count, dtype, n));
+  TRY(tensors(out, count, out_dtype, n));
+  if (!norm || off4(norm) || !(max_norm >= 0.0f)) return INSTANT_E_ARG;
+  TRY(workspace_ok(workspace, workspace_bytes, grad_norm_bytes(n)));
+  try {
+    if (outputs_overlap(grads, out, count, dtype, out_dtype, n)) return INSTANT_E_ARG;
+  } catch (const std::bad_alloc&) {
+    return INSTANT_E_HIP;
+  }
+  return hip_ok(launch_clip_grads(grads, count, dtype, out, out_dtype, n, max_norm, norm, workspace, S(stream)));
 }

@@ -1,5 +1,7 @@
 """Operators around the linear layer: its forward with bias, activation and residual, its exact
-backward from activations kept in 8 bits, and the RMS norm that feeds it (C ABI:
+backward from activations kept in 8 bits, and the RMS norm that feeds it; and operators at the
+ends of a language model's training step: the embedding and its gradient, log probabilities from
+logits and their gradient, the norm over all gradients and clipping (C ABI:
 ``include/instant_ops.h``, kernels in ``libinstant.so``).
 
 The ``instant_*`` functions marshal arguments to the C entry points of the same names. The
@@ -7,13 +9,14 @@ functions below them take and return torch tensors: they check shapes, types and
 allocate outputs and workspace (from torch's allocator, on the current stream) and raise
 ``ValueError``, ``TypeError`` or ``InstantError``. Leading dimensions count as rows: x [..., K]
 is a matrix of M rows. Inputs are contiguous, on the current device, and the work is enqueued
-on its current stream. None of them is differentiable by itself: ``linear.py`` and ``norm.py``
-build the layers.
+on its current stream. None of them is differentiable by itself: ``linear.py``, ``norm.py``,
+``embedding.py`` and ``loss.py`` build the layers.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,7 +28,13 @@ CKPT_GROUP = 32
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _DTYPES = {torch.float32: INSTANT_FP32, torch.bfloat16: INSTANT_BF16}
 
+IGNORE = -100  # the target of a row without a token
+MAX_VOCAB = 1 << 18
+MAX_TOP = 32
+_TOKENS = {torch.int64: 8, torch.int32: 4}
+
 _vp, _i, _sz, _st = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+_f, _l = ctypes.c_float, ctypes.c_int64
 _sig = {
     "instant_ckpt_pack": (_st, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "instant_ckpt_unpack": (_st, [_vp, _vp, _i, _i, _i, _vp, _vp]),
@@ -41,11 +50,19 @@ _sig = {
     "instant_rmsnorm_fwd": (_st, [_vp] * 3 + [_i] * 3 + [ctypes.c_float] + [_vp] * 6),
     "instant_rmsnorm_workspace_bytes": (_sz, [_i, _i]),
     "instant_rmsnorm_bwd": (_st, [_vp] * 5 + [_i] * 3 + [_vp] * 3 + [_sz, _vp]),
+    "instant_embed_fwd": (_st, [_vp, _i, _i, _vp, _i, _i, _i, _f, _vp, _vp]),
+    "instant_embed_workspace_bytes": (_sz, [_i, _i, _i]),
+    "instant_embed_bwd": (_st, [_vp, _vp] + [_i] * 5 + [_f, _l, _i, _vp, _vp, _sz, _vp]),
+    "instant_logprobs_fwd": (_st, [_vp, _vp] + [_i] * 5 + [_l, _i] + [_vp] * 7),
+    "instant_logprobs_bwd": (_st, [_vp, _vp] + [_i] * 5 + [_l] + [_vp] * 7),
+    "instant_grad_norm_workspace_bytes": (_sz, [_i]),
+    "instant_grad_norm": (_st, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "instant_clip_grads": (_st, [_vp] * 5 + [_i, _f, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
-    _f = getattr(_lib, _name)
-    _f.restype = _res
-    _f.argtypes = _args
+    _fn = getattr(_lib, _name)
+    _fn.restype = _res
+    _fn.argtypes = _args
 
 EXPORTED = tuple(_sig)
 
@@ -114,6 +131,59 @@ def instant_rmsnorm_bwd(gy, h, g, rstd, gh, M, C, dtype, gx, gg, workspace, work
                                     _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+def instant_embed_fwd(tokens, token_bytes, M, table, V, C, dtype, scale, y, stream=None) -> int:
+    return _lib.instant_embed_fwd(_ptr(tokens), token_bytes, M, _ptr(table), V, C, dtype, scale, _ptr(y),
+                                  _stream(stream))
+
+
+def instant_embed_workspace_bytes(M, V, C) -> int:
+    return int(_lib.instant_embed_workspace_bytes(M, V, C))
+
+
+def instant_embed_bwd(gy, tokens, token_bytes, M, V, C, dtype, scale, padding, accumulate, gtable, workspace,
+                      workspace_bytes, stream=None) -> int:
+    return _lib.instant_embed_bwd(_ptr(gy), _ptr(tokens), token_bytes, M, V, C, dtype, scale, padding, int(accumulate),
+                                  _ptr(gtable), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def instant_logprobs_fwd(logits, targets, token_bytes, M, W, V, dtype, ignore, k, logp, lse, entropy, stats, top_logp,
+                         top_index, stream=None) -> int:
+    return _lib.instant_logprobs_fwd(_ptr(logits), _ptr(targets), token_bytes, M, W, V, dtype, ignore, k, _ptr(logp),
+                                     _ptr(lse), _ptr(entropy), _ptr(stats), _ptr(top_logp), _ptr(top_index),
+                                     _stream(stream))
+
+
+def instant_logprobs_bwd(logits, targets, token_bytes, M, W, V, dtype, ignore, stats, entropy, g_logp, g_lse,
+                         g_entropy, gz, stream=None) -> int:
+    return _lib.instant_logprobs_bwd(_ptr(logits), _ptr(targets), token_bytes, M, W, V, dtype, ignore, _ptr(stats),
+                                     _ptr(entropy), _ptr(g_logp), _ptr(g_lse), _ptr(g_entropy), _ptr(gz),
+                                     _stream(stream))
+
+
+def _host(kind, values):
+    """A host array of the call (NULL for None)."""
+    return None if values is None else (kind * len(values))(*values)
+
+
+def instant_grad_norm_workspace_bytes(n) -> int:
+    return int(_lib.instant_grad_norm_workspace_bytes(n))
+
+
+def instant_grad_norm(grads, count, dtype, n, norm, workspace, workspace_bytes, stream=None) -> int:
+    """grads (tensors or addresses), count and dtype are sequences of n."""
+    return _lib.instant_grad_norm(_host(_vp, None if grads is None else [_ptr(g) for g in grads]), _host(_l, count),
+                                  _host(_i, dtype), n, _ptr(norm), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def instant_clip_grads(grads, count, dtype, out, out_dtype, n, max_norm, norm, workspace, workspace_bytes,
+                       stream=None) -> int:
+    """grads, count, dtype, out and out_dtype are sequences of n."""
+    g, o = (None if t is None else [_ptr(x) for x in t] for t in (grads, out))
+    return _lib.instant_clip_grads(_host(_vp, g), _host(_l, count), _host(_i, dtype), _host(_vp, o),
+                                   _host(_i, out_dtype), n, max_norm, _ptr(norm), _ptr(workspace), workspace_bytes,
+                                   _stream(stream))
+
+
 # ----------------------------------------------------------------------------- checks
 
 def _ok(status, where):
@@ -170,12 +240,41 @@ def _like(t, shape, dtype, device, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _tokens(t, name):
+    """Bytes of an integer of a token tensor."""
+    if not isinstance(t, Tensor):
+        _foreign(t, name)
+    size = _TOKENS.get(t.dtype)
+    if size is None:
+        raise TypeError(f"{name} must be int64 or int32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return size
+
+
+def _beside(t, shape, device, name):
+    """A token tensor beside the first tensor of the call."""
+    size = _tokens(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    return size
+
+
+def _finite(v, name):
+    if not math.isfinite(v) or abs(v) > 3.4028234663852886e38:
+        raise ValueError(f"{name} must be a finite float32, got {v}")
+
+
 # Sizes depend on the shapes alone.
 _fwd_bytes = functools.lru_cache(4096)(instant_linear_fwd_workspace_bytes)
 _gx_bytes = functools.lru_cache(4096)(instant_linear_gx_workspace_bytes)
 _gw_bytes = functools.lru_cache(4096)(instant_linear_gw_workspace_bytes)
 _act_bytes = functools.lru_cache(4096)(instant_act_bwd_workspace_bytes)
 _norm_bytes = functools.lru_cache(4096)(instant_rmsnorm_workspace_bytes)
+_embed_bytes = functools.lru_cache(4096)(instant_embed_workspace_bytes)
+_grads_bytes = functools.lru_cache(4096)(instant_grad_norm_workspace_bytes)
 
 
 def _workspace(n, like):
@@ -429,3 +528,217 @@ def rmsnorm_backward(gy, h, weight, rstd, gh=None, need_gweight=True):
     _ok(_lib.instant_rmsnorm_bwd(gy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _p(gh), M, C, dt,
                                  gx.data_ptr(), _p(gw), wp, n, _current(dev)), "instant_rmsnorm_bwd")
     return gx, gw
+
+
+# ----------------------------------------------------------------------------- embedding
+
+def embedding_forward(tokens, table, scale=1.0):
+    """y = scale * table[tokens] [..., C] for tokens [...] (int64 or int32) and table [V, C]. A
+    token outside 0 .. V - 1 gives a row of NaN."""
+    size = _tokens(tokens, "tokens")
+    dt = _dtype(table, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table must be [V, C], got {tuple(table.shape)}")
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    V, C = table.shape
+    _vocab(V, "table")
+    if C < 8 or C % 8:
+        raise ValueError(f"table's last dimension must be a positive multiple of 8, got {C}")
+    _finite(scale, "scale")
+    M = tokens.numel()
+    if M > 1 << 26:
+        raise ValueError(f"tokens are {M}, more than 2^26")
+    _on_device(table, "table")
+    dev = table.get_device()
+    if tokens.get_device() != dev:
+        raise ValueError(f"tokens must be on the current CUDA device, got {tokens.device}")
+    y = table.new_empty((*tokens.shape, C))
+    _ok(_lib.instant_embed_fwd(tokens.data_ptr(), size, M, table.data_ptr(), V, C, dt, scale, y.data_ptr(),
+                               _current(dev)), "instant_embed_fwd")
+    return y
+
+
+def _vocab(V, name):
+    if not 1 <= V <= MAX_VOCAB:
+        raise ValueError(f"{name}: a vocabulary is of 1 to {MAX_VOCAB} tokens, got {V}")
+
+
+def embedding_backward(gy, tokens, vocab, scale=1.0, padding=None, into=None):
+    """The table's gradient [vocab, C]: scale * the sums of gy's rows [..., C] by their tokens
+    [...], in the order of the rows; rows of the token `padding` take no part, nor does a token
+    outside the vocabulary. into: a gradient [vocab, C] that the sums are added to, in place (rows
+    without a token are not touched), and which is returned. At most 2^22 tokens."""
+    M, C, dt = _matrix(gy, "gy")
+    dev = gy.get_device()
+    size = _beside(tokens, gy.shape[:-1], dev, "tokens")
+    _vocab(vocab, "vocab")
+    _finite(scale, "scale")
+    if padding is None:
+        padding = -1
+    elif not 0 <= padding < vocab:
+        raise ValueError(f"padding must be a token of the vocabulary, got {padding}")
+    if M > 1 << 22:
+        raise ValueError(f"gy has {M} rows, more than 2^22")
+    if into is not None:
+        _like(into, (vocab, C), gy.dtype, dev, "into")
+    gw = gy.new_empty((vocab, C)) if into is None else into
+    n = _embed_bytes(M, vocab, C)
+    ws, wp = _workspace(n, gy)
+    _ok(_lib.instant_embed_bwd(gy.data_ptr(), tokens.data_ptr(), size, M, vocab, C, dt, scale, padding,
+                               into is not None, gw.data_ptr(), wp, n, _current(dev)), "instant_embed_bwd")
+    return gw
+
+
+# ----------------------------------------------------------------------------- log probabilities
+
+class TokenLogprobs(NamedTuple):
+    """Of logits [..., W] (float32 but for the places): logp, the log probability of the target
+    (None without targets), lse = log sum exp, entropy [...]; the alternatives' top_logp and
+    top_index (int64) [..., k], likeliest first (None unless asked for); stats [..., 2], what the
+    gradient needs."""
+    logp: Optional[torch.Tensor]
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_logp: Optional[torch.Tensor]
+    top_index: Optional[torch.Tensor]
+    stats: torch.Tensor
+
+
+def _logits(z, vocab):
+    """(rows, width, vocabulary, dtype code) of logits, whose rows may have any width."""
+    dt = _dtype(z, "logits")
+    if z.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    if not z.is_contiguous():
+        raise ValueError("logits must be contiguous")
+    W = z.shape[-1]
+    _vocab(W, "logits")
+    V = W if vocab is None else vocab
+    if not 1 <= V <= W:
+        raise ValueError(f"vocab must be 1 to the {W} columns of logits, got {V}")
+    M = z.numel() // W
+    if M > 1 << 26:
+        raise ValueError(f"logits have {M} rows, more than 2^26")
+    _on_device(z, "logits")
+    return M, W, V, dt
+
+
+def _int64(v, name):
+    if not -(1 << 63) <= v < 1 << 63:
+        raise ValueError(f"{name} must be an int64, got {v}")
+
+
+def token_logprobs(logits, targets=None, vocab=None, top=0, ignore=IGNORE) -> TokenLogprobs:
+    """Log probabilities of the tokens targets [...] (int64 or int32) under logits [..., W], the
+    entropy, and the `top` <= 32 likeliest alternatives (equal logits by their place). vocab: only
+    the first vocab columns count (a padded vocabulary). Where the target is `ignore` its log
+    probability is 0; where it is outside the vocabulary, NaN. A logit of -inf has probability 0;
+    a row of nothing else has lse -inf and entropy 0."""
+    M, W, V, dt = _logits(logits, vocab)
+    shape, dev = logits.shape[:-1], logits.get_device()
+    size = 8 if targets is None else _beside(targets, shape, dev, "targets")
+    if not 0 <= top <= min(MAX_TOP, V):
+        raise ValueError(f"top must be 0 to {min(MAX_TOP, V)}, got {top}")
+    _int64(ignore, "ignore")
+    logp = logits.new_empty(shape, dtype=torch.float32) if targets is not None else None
+    lse, entropy = (logits.new_empty(shape, dtype=torch.float32) for _ in range(2))
+    stats = logits.new_empty((*shape, 2), dtype=torch.float32)
+    tl = ti = None
+    if top:
+        tl = logits.new_empty((*shape, top), dtype=torch.float32)
+        ti = logits.new_empty((*shape, top), dtype=torch.int64)
+    _ok(_lib.instant_logprobs_fwd(logits.data_ptr(), _p(targets), size, M, W, V, dt, ignore, top, _p(logp),
+                                  lse.data_ptr(), entropy.data_ptr(), stats.data_ptr(), _p(tl), _p(ti),
+                                  _current(dev)), "instant_logprobs_fwd")
+    return TokenLogprobs(logp, lse, entropy, tl, ti, stats)
+
+
+def token_logprobs_backward(logits, targets, stats, g_logp=None, g_lse=None, g_entropy=None, entropy=None, vocab=None,
+                            ignore=IGNORE, in_place=False):
+    """The gradient of logits (of their shape and type) for the gradients g_logp, g_lse and
+    g_entropy [...] of token_logprobs' results, with its stats and (for g_entropy) its entropy:
+    g_logp (1[j = target] - p) + g_lse p - g_entropy p (log p + entropy), zeros behind the
+    vocabulary. A row whose gradients are all 0 gets zeros, whatever it holds. in_place: it is
+    written over logits and logits are returned."""
+    M, W, V, dt = _logits(logits, vocab)
+    shape, dev = logits.shape[:-1], logits.get_device()
+    if g_logp is None and g_lse is None and g_entropy is None:
+        raise ValueError("one of g_logp, g_lse and g_entropy has to be given")
+    if targets is None and g_logp is not None:
+        raise ValueError("targets are needed for g_logp")
+    if entropy is None and g_entropy is not None:
+        raise ValueError("entropy is needed for g_entropy")
+    size = 8 if targets is None else _beside(targets, shape, dev, "targets")
+    _like(stats, (*shape, 2), torch.float32, dev, "stats")
+    for t, name in ((g_logp, "g_logp"), (g_lse, "g_lse"), (g_entropy, "g_entropy"), (entropy, "entropy")):
+        if t is not None:
+            _like(t, shape, torch.float32, dev, name)
+    _int64(ignore, "ignore")
+    gz = logits if in_place else torch.empty_like(logits)
+    _ok(_lib.instant_logprobs_bwd(logits.data_ptr(), _p(targets), size, M, W, V, dt, ignore, stats.data_ptr(),
+                                  _p(entropy), _p(g_logp), _p(g_lse), _p(g_entropy), gz.data_ptr(), _current(dev)),
+        "instant_logprobs_bwd")
+    return gz
+
+
+# ----------------------------------------------------------------------------- gradients of a model
+
+def _grads(tensors, name):
+    """(tensors as a list, and of each the address, the elements and the dtype code)."""
+    if isinstance(tensors, Tensor):
+        raise TypeError(f"{name} must be a sequence of tensors, got a tensor")
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError(f"{name} must hold a tensor at least")
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    at, count, codes = [], [], []
+    for t in tensors:
+        codes.append(_dtype(t, name))
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        at.append(t.data_ptr())
+        count.append(t.numel())
+    return tensors, at, count, codes
+
+
+def grad_norm(tensors) -> torch.Tensor:
+    """The Euclidean norm over all elements of a sequence of tensors (float32 and bfloat16 in any
+    mixture, of any shapes), a float32 scalar on the device. Squares are summed in float64."""
+    tensors, at, count, codes = _grads(tensors, "tensors")
+    n, first = len(tensors), tensors[0]
+    norm = first.new_empty((), dtype=torch.float32)
+    size = _grads_bytes(n)
+    ws, wp = _workspace(size, first)
+    _ok(_lib.instant_grad_norm(_host(_vp, at), _host(_l, count), _host(_i, codes), n, norm.data_ptr(), wp, size,
+                               _current(first.get_device())), "instant_grad_norm")
+    return norm
+
+
+def clip_grads(tensors, max_norm, out=None) -> torch.Tensor:
+    """Scales a sequence of tensors so that the norm over all their elements is at most max_norm:
+    by max_norm / (norm + 1e-6) where that is below 1, else not at all. Returns the norm before (a
+    float32 scalar on the device; nothing waits for it). out: tensors of the same shapes, float32 or
+    bfloat16, that receive the result; None: the tensors themselves. Outputs may not share memory
+    with each other or with another tensor of the call."""
+    tensors, at, count, codes = _grads(tensors, "tensors")
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm must not be negative, got {max_norm}")
+    n, first = len(tensors), tensors[0]
+    to, to_codes = at, codes
+    if out is not None:
+        out, to, _, to_codes = _grads(out, "out")
+        if len(out) != n:
+            raise ValueError(f"out must hold {n} tensors, got {len(out)}")
+        for t, o in zip(tensors, out):
+            if t.shape != o.shape:
+                raise ValueError(f"out must have the tensors' shapes, got {tuple(o.shape)} for {tuple(t.shape)}")
+    norm = first.new_empty((), dtype=torch.float32)
+    size = _grads_bytes(n)
+    ws, wp = _workspace(size, first)
+    _ok(_lib.instant_clip_grads(_host(_vp, at), _host(_l, count), _host(_i, codes), _host(_vp, to), _host(_i, to_codes),
+                                n, max_norm, norm.data_ptr(), wp, size, _current(first.get_device())),
+        "instant_clip_grads")
+    return norm
