@@ -363,7 +363,8 @@ def check_embed_back(gy, t, V, scale, padding, into=None):
 
 EMBED_SHAPES = [(1, 1, 8), (1, 1000, 64), (2, 3, 8), (8, 128000, 512), (31, 50, 136), (32, 7, 64), (33, 5, 72),
                 (100, 1, 128), (1000, 30522, 768), (4095, 97, 264), (4096, 4096, 64), (4097, 300, 2056),
-                (9000, 262144, 8), (16384, 32000, 128), (20000, 2, 40)]
+                (9000, 262144, 8), (16384, 32000, 128), (20000, 2, 40),
+                (1024, 5000, 16), (1025, 1025, 24), (2049, 262144, 8)]
 
 
 @DTYPES
