@@ -33,8 +33,8 @@ template <class T> using vec8_t = typename MM<T>::vec8;
 
 }  // namespace
 
-// TPR threads a row of U units of 8 columns, 256 / TPR rows a block.
-template <class T, int TPR>
+// TPR threads a row, UNITS units of 8 columns a thread, 256 / TPR rows a block.
+template <class T, int TPR, int UNITS>
 __global__ __launch_bounds__(256) void embed_kernel(const void* __restrict__ tokens, bool wide, int M,
                                                     const T* __restrict__ w, int V, int C, float scale,
                                                     T* __restrict__ y) {
@@ -45,12 +45,18 @@ __global__ __launch_bounds__(256) void embed_kernel(const void* __restrict__ tok
     const bool in = t >= 0 && t < V;
     const T* row = w + (in ? (size_t)t * C : 0);
     T* out = y + (size_t)m * C;
-    for (int n = 8 * i; n < C; n += 8 * TPR) {
-      float v[8];
-      load8(row + n, v);
+    for (int n0 = 8 * i; n0 < C; n0 += 8 * TPR * UNITS) {
+      vec8_t<T> v[UNITS];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = in ? v[j] * scale : NAN;
-      store_row<T, 8>(out + n, v);
+      for (int k = 0; k < UNITS; ++k)
+        v[k] = *reinterpret_cast<const vec8_t<T>*>(row + (n0 + 8 * TPR * k < C ? n0 + 8 * TPR * k : n0));
+#pragma unroll
+      for (int k = 0; k < UNITS; ++k) {
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = in ? (float)v[k][j] * scale : NAN;
+        if (n0 + 8 * TPR * k < C) store_row<T, 8>(out + n0 + 8 * TPR * k, o);
+      }
     }
   }
 }
@@ -323,7 +329,7 @@ __global__ __launch_bounds__(256) void group_kernel(const void* __restrict__ tok
   for (int r = tid / tpr; r < rows; r += 256 / tpr) {
     const size_t v = (size_t)r * CLASSES + b;
     if (v >= (size_t)V || counts[0][r]) continue;
-    for (int k = tid % tpr; k < units; k += tpr) fill[v * units + k] = uint4{0, 0, 0, 0};
+    for (int k = tid % tpr; k < units; k += tpr) __builtin_nontemporal_store(zero4(), (f32x4*)fill + v * units + k);
   }
 }
 
@@ -441,14 +447,18 @@ __global__ __launch_bounds__(SUM_WAVES* WAVE) void run_join_kernel(Grouped group
   const unsigned t = grouped.token[last];
   if (grouped.token[last + 1] != t) return;
   if (tile > 0 && grouped.token[last - TILE] == t) return;  // it came from the tile before
-  // tiles that go on with it: those that begin with it (a binary search, as equal tokens are together)
-  int end = tile + 2, hi = (M + TILE - 1) / TILE;
-  while (end < hi) {
-    const int mid = (end + hi) / 2;
-    if (grouped.token[(size_t)mid * TILE] == t) end = mid + 1;
-    else hi = mid;
-  }
+  // tiles that go on with it: those that begin with it, looked up 64 at a time
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, col = 8 * (WAVE * blockIdx.y + lane);
+  int end = tile + 1;
+  while (true) {
+    const int64_t at = (int64_t)(end + lane) * TILE;
+    const uint64_t other = __ballot(!(at < M && grouped.token[at] == t));
+    if (other) {
+      end += __ffsll((unsigned long long)other) - 1;
+      break;
+    }
+    end += WAVE;
+  }
   const bool in = col < C;
   const int64_t n = end - tile;  // partial rows
   const int u0 = tile + (int)(n * wave / SUM_WAVES), u1 = tile + (int)(n * (wave + 1) / SUM_WAVES);
@@ -534,12 +544,14 @@ template <class T>
 hipError_t embed_fwd(const void* tokens, bool wide, int M, const void* w, int V, int C, float scale, void* y,
                      hipStream_t st) {
   const int u = C / 8;
-#define FWD(TPR)                                                                                                   \
-  hipLaunchKernelGGL((embed_kernel<T, TPR>), dim3(std::min((M + 256 / TPR - 1) / (256 / TPR), 1 << 20)), dim3(256), \
-                     0, st, tokens, wide, M, (const T*)w, V, C, scale, (T*)y)
-  if (u <= 16) FWD(16);
-  else if (u <= 64) FWD(64);
-  else FWD(256);
+#define FWD(TPR, UNITS)                                                                                              \
+  hipLaunchKernelGGL((embed_kernel<T, TPR, UNITS>), dim3(std::min((M + 256 / TPR - 1) / (256 / TPR), 1 << 20)), \
+                     dim3(256), 0, st, tokens, wide, M, (const T*)w, V, C, scale, (T*)y)
+  if (u <= 16) FWD(16, 1);
+  else if (u <= 64) FWD(64, 1);
+  else if (u <= 128) FWD(64, 2);
+  else if (u <= 256) FWD(64, 4);
+  else FWD(128, 4);
 #undef FWD
   return hipGetLastError();
 }
