@@ -156,6 +156,10 @@ instant_status instant_embed_bwd(const void* gy, const void* tokens, int32_t tok
                                  int32_t C, int32_t dtype, float scale, int64_t padding, int32_t accumulate,
                                  void* gtable, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace for instant_logprobs_fwd (0: nothing, or sizes that are not accepted): few
+ * long rows are split. */
+size_t instant_logprobs_workspace_bytes(int32_t M, int32_t V, int32_t dtype, int32_t k);
+
 /* Log probabilities from logits [M, W], of whose columns the first V <= W <= 2^18 count. Each of
  *   logp     float [M]     log of the probability of targets[m]; 0 where that is `ignore`
  *   lse      float [M]     log sum exp(logits)
@@ -171,7 +175,7 @@ instant_status instant_embed_bwd(const void* gy, const void* tokens, int32_t tok
 instant_status instant_logprobs_fwd(const void* logits, const void* targets, int32_t token_bytes, int32_t M,
                                     int32_t W, int32_t V, int32_t dtype, int64_t ignore, int32_t k, float* logp,
                                     float* lse, float* entropy, float* stats, float* top_logp, int64_t* top_index,
-                                    void* stream);
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* The logits' gradient gz [M, W] for gradients g_logp, g_lse, g_entropy [M] (each may be NULL, not
  * all) of logp, lse and entropy, with stats and (for g_entropy) entropy from the forward pass:

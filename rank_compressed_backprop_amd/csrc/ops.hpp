@@ -320,10 +320,11 @@ hipError_t launch_embed_bwd(bool bf16_io, const void* gy, const void* tokens, bo
                             float scale, int64_t padding, bool add, void* gw, void* ws, hipStream_t st);
 
 constexpr int LOGPROBS_MAX_TOP = 32;
+size_t logprobs_fwd_bytes(bool bf16_io, int M, int V, int k);
 // Logits [M][W], of which the first V columns count; outputs that are null are not written.
 hipError_t launch_logprobs_fwd(bool bf16_io, const void* z, const void* targets, bool wide, int M, int W, int V,
                                int64_t ignore, int k, float* logp, float* lse, float* entropy, float* stats,
-                               float* top_logp, int64_t* top_index, hipStream_t st);
+                               float* top_logp, int64_t* top_index, void* ws, hipStream_t st);
 hipError_t launch_logprobs_bwd(bool bf16_io, const void* z, const void* targets, bool wide, int M, int W, int V,
                                int64_t ignore, const float* stats, const float* entropy, const float* g_logp,
                                const float* g_lse, const float* g_ent, void* gz, hipStream_t st);

@@ -295,10 +295,16 @@ INSTANT_API instant_status instant_embed_bwd(const void* gy, const void* tokens,
                                  accumulate != 0, gtable, workspace, S(stream)));
 }
 
+INSTANT_API size_t instant_logprobs_workspace_bytes(int32_t M, int32_t V, int32_t dtype, int32_t k) {
+  if (vocab(M, V, V) != INSTANT_OK || !dtype_ok(dtype) || k < 0 || k > LOGPROBS_MAX_TOP || k > V) return 0;
+  return logprobs_fwd_bytes(dtype == INSTANT_BF16, M, V, k);
+}
+
 INSTANT_API instant_status instant_logprobs_fwd(const void* logits, const void* targets, int32_t token_bytes,
                                                 int32_t M, int32_t W, int32_t V, int32_t dtype, int64_t ignore,
                                                 int32_t k, float* logp, float* lse, float* entropy, float* stats,
-                                                float* top_logp, int64_t* top_index, void* stream) {
+                                                float* top_logp, int64_t* top_index, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
   TRY(vocab(M, W, V));
   if (!dtype_ok(dtype) || !tokens_ok(targets, token_bytes) || !logits_ok(logits, dtype) ||
       off4(logp, lse, entropy, stats, top_logp) || ((uintptr_t)top_index) % 8)
@@ -309,8 +315,10 @@ INSTANT_API instant_status instant_logprobs_fwd(const void* logits, const void* 
   if (!logits || (targets == nullptr) != (logp == nullptr)) return INSTANT_E_ARG;
   if ((k > 0) != (top_logp != nullptr) || (k > 0) != (top_index != nullptr)) return INSTANT_E_ARG;
   if (!logp && !lse && !entropy && !stats && !k) return INSTANT_E_ARG;
-  return hip_ok(launch_logprobs_fwd(dtype == INSTANT_BF16, logits, targets, token_bytes == 8, M, W, V, ignore, k, logp,
-                                    lse, entropy, stats, top_logp, top_index, S(stream)));
+  const bool bf = dtype == INSTANT_BF16;
+  TRY(workspace_ok(workspace, workspace_bytes, logprobs_fwd_bytes(bf, M, V, k)));
+  return hip_ok(launch_logprobs_fwd(bf, logits, targets, token_bytes == 8, M, W, V, ignore, k, logp, lse, entropy,
+                                    stats, top_logp, top_index, workspace, S(stream)));
 }
 
 INSTANT_API instant_status instant_logprobs_bwd(const void* logits, const void* targets, int32_t token_bytes,

@@ -53,7 +53,8 @@ _sig = {
     "instant_embed_fwd": (_st, [_vp, _i, _i, _vp, _i, _i, _i, _f, _vp, _vp]),
     "instant_embed_workspace_bytes": (_sz, [_i, _i, _i]),
     "instant_embed_bwd": (_st, [_vp, _vp] + [_i] * 5 + [_f, _l, _i, _vp, _vp, _sz, _vp]),
-    "instant_logprobs_fwd": (_st, [_vp, _vp] + [_i] * 5 + [_l, _i] + [_vp] * 7),
+    "instant_logprobs_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "instant_logprobs_fwd": (_st, [_vp, _vp] + [_i] * 5 + [_l, _i] + [_vp] * 7 + [_sz, _vp]),
     "instant_logprobs_bwd": (_st, [_vp, _vp] + [_i] * 5 + [_l] + [_vp] * 7),
     "instant_grad_norm_workspace_bytes": (_sz, [_i]),
     "instant_grad_norm": (_st, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
@@ -146,11 +147,15 @@ def instant_embed_bwd(gy, tokens, token_bytes, M, V, C, dtype, scale, padding, a
                                   _ptr(gtable), _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+def instant_logprobs_workspace_bytes(M, V, dtype, k) -> int:
+    return int(_lib.instant_logprobs_workspace_bytes(M, V, dtype, k))
+
+
 def instant_logprobs_fwd(logits, targets, token_bytes, M, W, V, dtype, ignore, k, logp, lse, entropy, stats, top_logp,
-                         top_index, stream=None) -> int:
+                         top_index, workspace, workspace_bytes, stream=None) -> int:
     return _lib.instant_logprobs_fwd(_ptr(logits), _ptr(targets), token_bytes, M, W, V, dtype, ignore, k, _ptr(logp),
                                      _ptr(lse), _ptr(entropy), _ptr(stats), _ptr(top_logp), _ptr(top_index),
-                                     _stream(stream))
+                                     _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def instant_logprobs_bwd(logits, targets, token_bytes, M, W, V, dtype, ignore, stats, entropy, g_logp, g_lse,
@@ -273,6 +278,7 @@ _gx_bytes = functools.lru_cache(4096)(instant_linear_gx_workspace_bytes)
 _gw_bytes = functools.lru_cache(4096)(instant_linear_gw_workspace_bytes)
 _act_bytes = functools.lru_cache(4096)(instant_act_bwd_workspace_bytes)
 _norm_bytes = functools.lru_cache(4096)(instant_rmsnorm_workspace_bytes)
+_logprobs_bytes = functools.lru_cache(4096)(instant_logprobs_workspace_bytes)
 _embed_bytes = functools.lru_cache(4096)(instant_embed_workspace_bytes)
 _grads_bytes = functools.lru_cache(4096)(instant_grad_norm_workspace_bytes)
 
@@ -648,8 +654,10 @@ def token_logprobs(logits, targets=None, vocab=None, top=0, ignore=IGNORE) -> To
     if top:
         tl = logits.new_empty((*shape, top), dtype=torch.float32)
         ti = logits.new_empty((*shape, top), dtype=torch.int64)
+    n = _logprobs_bytes(M, V, dt, top)
+    ws, wp = _workspace(n, logits)
     _ok(_lib.instant_logprobs_fwd(logits.data_ptr(), _p(targets), size, M, W, V, dt, ignore, top, _p(logp),
-                                  lse.data_ptr(), entropy.data_ptr(), stats.data_ptr(), _p(tl), _p(ti),
+                                  lse.data_ptr(), entropy.data_ptr(), stats.data_ptr(), _p(tl), _p(ti), wp, n,
                                   _current(dev)), "instant_logprobs_fwd")
     return TokenLogprobs(logp, lse, entropy, tl, ti, stats)
 

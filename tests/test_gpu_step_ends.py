@@ -300,8 +300,11 @@ def test_gradient_in_place_and_inside(m, v, dtype):
     assert s == 0 and bool((dst[n:] == 7.0).all())
     held = [torch.full((m * w + 32,), 7.0, device="cuda") for w in (1, 1, 1, 2, 3)]
     idx = torch.full((m * 3 + 32,), 7, device="cuda")
-    s = ops.instant_logprobs_fwd(apart, t, 8, m, v, v, int(dtype == BF), -100, 3, *held, idx)
+    need = ops.instant_logprobs_workspace_bytes(m, v, int(dtype == BF), 3)
+    ws = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
+    s = ops.instant_logprobs_fwd(apart, t, 8, m, v, v, int(dtype == BF), -100, 3, *held, idx, ws, need)
     torch.cuda.synchronize()
+    assert bool((ws[need:] == 7).all())
     assert s == 0 and all(bool((h[m * w:] == 7.0).all()) for h, w in zip(held, (1, 1, 1, 2, 3)))
     assert bool((idx[m * 3:] == 7).all())
 
