@@ -271,7 +271,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void logprobs_kernel(
   static_assert(TPR >= WAVE || TOP < 2, "ranking takes a wave");
   // few rows: a block goes through its code once or twice, and most of its time is the code's way from
   // memory, so every chunk takes the same short loop (64 x 128000: 14 us, with steps of U chunks 18)
-  constexpr bool SMALL = SPLIT || TPR == 1024;
+  constexpr bool SMALL = TPR == 1024;
   __shared__ float sums[RPB][3][WAVES];
   __shared__ uint64_t groups_[TOP == 2 ? RPB : 1][64], cand_[TOP == 2 ? RPB : 1][TOP == 2 ? CANDS + PAD : 1];
   __shared__ uint64_t bound_[RPB];
@@ -668,11 +668,13 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
 
 namespace {
 
-// Slices of a row (1: not split): for few rows of many chunks, enough blocks for the chip.
-int slices_of(bool bf16_io, int M, int V) {
+// Slices of a row (1: not split): for few rows of many chunks, a block of 1024 threads for each
+// compute unit, with at most 80 alternatives of a row to join. (64 x 128000 in float32, k = 0 and 20: 20
+// and 27 us in whole rows, 16 and 22 in 4 slices of 256 threads, 14 and 26 in 8.)
+int slices_of(bool bf16_io, int M, int V, int k) {
   const int chunks = V / (bf16_io ? 8 : 4);
-  if (M > 512 || chunks < 8192) return 1;
-  return std::max(1, std::min({MAX_SLICES, 1024 / std::max(M, 1), chunks / 512}));
+  if (M > 128 || chunks < 8192) return 1;
+  return std::max(1, std::min({MAX_SLICES, 256 / std::max(M, 1), chunks / 1024, 80 / std::max(k, 1)}));
 }
 
 struct Call {
@@ -699,12 +701,12 @@ template <class T, int TPR, int TOP> hipError_t run_fwd(const Call& c) {
 }
 
 template <class T, int TOP> hipError_t run_top(const Call& c, void* ws) {
-  const int slices = slices_of(sizeof(T) == 2, c.M, c.V), chunks = c.V / (16 / (int)sizeof(T));
+  const int slices = slices_of(sizeof(T) == 2, c.M, c.V, c.k), chunks = c.V / (16 / (int)sizeof(T));
   if (slices > 1) {
     uint64_t* keys = (uint64_t*)ws;
     float* parts = (float*)(keys + (size_t)c.M * slices * c.k);
-    const int steps = most_steps<T, 256>((chunks + 2) / slices + 1);
-    hipLaunchKernelGGL((logprobs_kernel<T, 256, TOP, true>), dim3(c.M * slices), dim3(256), (lds_bytes<256, TOP>(steps)),
+    const int steps = most_steps<T, 1024>((chunks + 2) / slices + 1);
+    hipLaunchKernelGGL((logprobs_kernel<T, 1024, TOP, true>), dim3(c.M * slices), dim3(1024), (lds_bytes<1024, TOP>(steps)),
                        c.st, (const T*)c.z, c.targets, c.wide, c.M, c.W, c.V, c.ignore, c.k, c.out, slices, parts, keys,
                        steps);
     hipLaunchKernelGGL((logprobs_join_kernel<T, TOP>), dim3(c.M), dim3(256), 0, c.st, (const T*)c.z, c.targets, c.wide,
@@ -737,7 +739,7 @@ hipError_t run_bwd(const void* z, const void* targets, bool wide, int M, int W, 
 }  // namespace
 
 size_t logprobs_fwd_bytes(bool bf16_io, int M, int V, int k) {
-  const size_t s = slices_of(bf16_io, M, V);
+  const size_t s = slices_of(bf16_io, M, V, k);
   return s > 1 ? (size_t)M * s * (8 * k + 12) : 0;
 }
 
