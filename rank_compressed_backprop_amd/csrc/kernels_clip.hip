@@ -16,7 +16,7 @@ namespace instant {
 
 namespace {
 
-constexpr int TENSORS = 96;       // a launch (of the 4 KB of arguments)
+constexpr int TENSORS = 120;      // a launch (of the 4 KB of arguments)
 constexpr int PIECE = 1 << 15;    // elements that a block takes at a time
 constexpr int GRID = 2048;        // blocks a launch at most
 constexpr float EPS = 1e-6f;
@@ -25,20 +25,20 @@ struct Table {
   const void* src[TENSORS];
   void* dst[TENSORS];
   int64_t count[TENSORS];
-  int64_t end[TENSORS];     // pieces of the tensors up to and with this one
+  uint32_t end[TENSORS];    // pieces of the tensors up to and with this one
   uint8_t bf[TENSORS];      // bit 0: src is bfloat16, bit 1: dst is
   int n;
 };
 
 // The tensor of piece p, and the piece's first element.
-__device__ __forceinline__ int find(const Table& t, int64_t p, int64_t& first) {
+__device__ __forceinline__ int find(const Table& t, uint32_t p, int64_t& first) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
     if (p < t.end[mid]) hi = mid;
     else lo = mid + 1;
   }
-  first = (p - (lo ? t.end[lo - 1] : 0)) * PIECE;
+  first = (int64_t)(p - (lo ? t.end[lo - 1] : 0)) * PIECE;
   return lo;
 }
 
@@ -77,14 +77,14 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void square_sum_kernel(Table t, int64_t pieces, double* __restrict__ part) {
+__global__ __launch_bounds__(256) void square_sum_kernel(Table t, uint32_t pieces, double* __restrict__ part) {
   __shared__ double lds[4];
   double sum = 0.0;
   auto add = [&](int, const float* v, auto n) {
 #pragma unroll
     for (int j = 0; j < decltype(n)::value; ++j) sum = fma((double)v[j], (double)v[j], sum);
   };
-  for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
+  for (uint32_t p = blockIdx.x; p < pieces; p += gridDim.x) {
     int64_t first;
     const int i = find(t, p, first);
     const int n = (int)min((int64_t)PIECE, t.count[i] - first);
@@ -95,18 +95,26 @@ __global__ __launch_bounds__(256) void square_sum_kernel(Table t, int64_t pieces
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// norm, and the factor for max_norm (NaN stays NaN; an infinite norm gives 0).
-__global__ __launch_bounds__(1024) void norm_kernel(const double* __restrict__ part, int n, float max_norm,
-                                                    float* __restrict__ norm, float* __restrict__ factor) {
-  __shared__ double lds[16];
+namespace {
+
+// The norm from the partial sums, by a block of 256 threads: every block's is the same.
+__device__ __forceinline__ float norm_of(const double* part, int n) {
+  __shared__ double lds[4];
   double sum = 0.0;
-  for (int i = threadIdx.x; i < n; i += 1024) sum += part[i];
-  sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) {
-    const float v = (float)sqrt(sum);
-    if (norm) *norm = v;
-    if (factor) *factor = v + EPS <= max_norm ? 1.0f : max_norm / (v + EPS);
-  }
+  for (int i = threadIdx.x; i < n; i += 256) sum += part[i];
+  return (float)sqrt(block_sum(sum, lds));
+}
+
+// NaN stays NaN; an infinite norm gives 0.
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  return norm + EPS <= max_norm ? 1.0f : max_norm / (norm + EPS);
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(256) void norm_kernel(const double* __restrict__ part, int n, float* __restrict__ norm) {
+  const float v = norm_of(part, n);
+  if (threadIdx.x == 0) *norm = v;
 }
 
 namespace {
@@ -136,11 +144,17 @@ __device__ __forceinline__ void scale_piece(const S* src, D* dst, int n, float c
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void scale_kernel(Table t, int64_t pieces, const float* __restrict__ factor) {
-  const float c = *factor;
-  for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
+// parts > 0: the norm from the partial sums (which a launch of its own would take 7 us for), which block 0
+// leaves at norm; else it is there. From the last piece to the first: the last ones' gradients are in the
+// cache.
+__global__ __launch_bounds__(256) void scale_kernel(Table t, uint32_t pieces, const double* __restrict__ part,
+                                                    int parts, float max_norm, float* norm) {
+  const float v = parts ? norm_of(part, parts) : *norm;
+  if (parts && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+  const float c = factor_of(v, max_norm);
+  for (uint32_t k = blockIdx.x; k < pieces; k += gridDim.x) {
     int64_t first;
-    const int i = find(t, p, first);
+    const int i = find(t, pieces - 1 - k, first);
     const int n = (int)min((int64_t)PIECE, t.count[i] - first);
     const bf16* sb = (const bf16*)t.src[i] + first;
     const float* sf = (const float*)t.src[i] + first;
@@ -159,54 +173,62 @@ namespace {
 
 int launches(int n) { return (n + TENSORS - 1) / TENSORS; }
 
-// Tensors [first, ...) of a launch; its pieces.
-int64_t fill(Table& t, const void* const* src, void* const* dst, const int64_t* count, const int32_t* bf,
-             const int32_t* dst_bf, int first, int n) {
+// Tensors [first, ...) of a launch; its pieces (at most 2^40 / PIECE for each: 32 bits hold them).
+uint32_t fill(Table& t, const void* const* src, void* const* dst, const int64_t* count, const int32_t* bf,
+              const int32_t* dst_bf, int first, int n) {
   t.n = std::min(TENSORS, n - first);
-  int64_t pieces = 0;
+  uint32_t pieces = 0;
   for (int i = 0; i < t.n; ++i) {
     const int k = first + i;
     t.src[i] = src[k];
     t.dst[i] = dst ? dst[k] : nullptr;
     t.count[i] = count[k];
-    pieces += (count[k] + PIECE - 1) / PIECE;
+    pieces += (uint32_t)((count[k] + PIECE - 1) / PIECE);
     t.end[i] = pieces;
     t.bf[i] = (uint8_t)((bf[k] ? 1 : 0) | (dst && dst_bf[k] ? 2 : 0));
   }
   return pieces;
 }
+static_assert((((int64_t)1 << 40) / PIECE) * TENSORS < (int64_t)1 << 32, "pieces");
 
-}  // namespace
-
-size_t grad_norm_bytes(int n) { return 256 + (size_t)launches(n) * GRID * sizeof(double); }
-
-hipError_t launch_grad_norm(const void* const* src, const int64_t* count, const int32_t* bf, int n, float max_norm,
-                            float* norm, void* ws, hipStream_t st, bool factor) {
-  double* part = (double*)((char*)ws + 256);
+// The partial sums of all tensors, and how many.
+int square_sums(const void* const* src, const int64_t* count, const int32_t* bf, int n, double* part, hipStream_t st) {
   int parts = 0;
   for (int k = 0; k < n; k += TENSORS) {
     Table t;
-    const int64_t pieces = fill(t, src, nullptr, count, bf, nullptr, k, n);
-    const int grid = (int)std::min<int64_t>(pieces, GRID);
+    const uint32_t pieces = fill(t, src, nullptr, count, bf, nullptr, k, n);
+    const int grid = (int)std::min<uint32_t>(pieces, GRID);
     if (!grid) continue;
     hipLaunchKernelGGL(square_sum_kernel, dim3(grid), dim3(256), 0, st, t, pieces, part + parts);
     parts += grid;
   }
-  hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(1024), 0, st, part, parts, max_norm, norm,
-                     factor ? (float*)ws : nullptr);
+  return parts;
+}
+
+}  // namespace
+
+size_t grad_norm_bytes(int n) { return std::max<size_t>(1, launches(n)) * GRID * sizeof(double); }
+
+hipError_t launch_grad_norm(const void* const* src, const int64_t* count, const int32_t* bf, int n, float* norm,
+                            void* ws, hipStream_t st) {
+  const int parts = square_sums(src, count, bf, n, (double*)ws, st);
+  hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(256), 0, st, (const double*)ws, parts, norm);
   return hipGetLastError();
 }
 
 hipError_t launch_clip_grads(const void* const* src, const int64_t* count, const int32_t* bf, void* const* dst,
                              const int32_t* dst_bf, int n, float max_norm, float* norm, void* ws, hipStream_t st) {
-  const hipError_t e = launch_grad_norm(src, count, bf, n, max_norm, norm, ws, st, true);
-  if (e != hipSuccess) return e;
+  int parts = square_sums(src, count, bf, n, (double*)ws, st);
+  if (n > TENSORS || !parts) {  // (several launches scale; or none)
+    hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(256), 0, st, (const double*)ws, parts, norm);
+    parts = 0;
+  }
   for (int k = 0; k < n; k += TENSORS) {
     Table t;
-    const int64_t pieces = fill(t, src, dst, count, bf, dst_bf, k, n);
+    const uint32_t pieces = fill(t, src, dst, count, bf, dst_bf, k, n);
     if (!pieces) continue;
-    hipLaunchKernelGGL(scale_kernel, dim3((unsigned)std::min<int64_t>(pieces, GRID)), dim3(256), 0, st, t, pieces,
-                       (const float*)ws);
+    hipLaunchKernelGGL(scale_kernel, dim3(std::min<uint32_t>(pieces, GRID)), dim3(256), 0, st, t, pieces,
+                       (const double*)ws, parts, max_norm, norm);
   }
   return hipGetLastError();
 }

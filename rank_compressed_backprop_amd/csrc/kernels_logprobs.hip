@@ -593,6 +593,9 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(const T* __restrict_
 // of them. A thread requests all its chunks before it stores one (gz may be z, so the compiler would
 // not); it writes the chunks that it has read.
 constexpr int BACK = 4;
+// A gradient that the 256 MB cache cannot hold for its reader is stored past the caches (8192 x 128000 in
+// bfloat16 817 -> 773 us; chunks two or eight at a time are no faster, nor is a grid that stays).
+constexpr size_t CACHE = (size_t)256 << 20;
 
 template <class T, int TPR>
 __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const void* __restrict__ targets, bool wide,
@@ -601,7 +604,7 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
                                                            const float* __restrict__ entropy,
                                                            const float* __restrict__ g_logp,
                                                            const float* __restrict__ g_lse,
-                                                           const float* __restrict__ g_ent, T* gz) {
+                                                           const float* __restrict__ g_ent, T* gz, bool past) {
   constexpr int CE = 16 / sizeof(T), PPB = 256 / TPR;
   const size_t units = (size_t)M * pieces;
   for (size_t u = (size_t)blockIdx.x * PPB + threadIdx.x / TPR; u < units; u += (size_t)gridDim.x * PPB) {
@@ -629,6 +632,12 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
     const bool empty = ls == -INFINITY;                         // p = 0
     const float base = gl - g - (gh != 0.0f ? gh * entropy[row] : 0.0f);
     const int tj = t >= 0 && t < V ? (int)t : -1;
+    // Without an entropy gradient a value is p * base, with p's exponent of two in two operations, or one
+    // for a bfloat16 result: fl(log2(e) (top + ls)) is off by 2^-24 of itself, and p by 2^-19 of itself
+    // where that is 30, against 2^-9 of the result's own rounding. (16384 x 30522 392 -> 387 us: bound by
+    // memory either way.)
+    const bool plain = gh == 0.0f && !empty && near(top);
+    const float m2 = top * LOG2E, l2 = fmaf(ls, LOG2E, rest(top)), both = m2 + l2;
 #pragma unroll
     for (int b = 0; b < BACK; ++b) {
       const int c = c0 + b * TPR, j0 = r.first(c);
@@ -641,11 +650,17 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
       } else {
         r.part(in, c, 0.0f, v);
       }
+      if (plain) {
 #pragma unroll
-      for (int j = 0; j < CE; ++j) {
-        const float lp = v[j] - top - ls;
-        const float p = empty ? 0.0f : exp_of(lp);
-        v[j] = p * fmaf(-gh, fmaxf(lp, FAR), base);
+        for (int j = 0; j < CE; ++j)
+          v[j] = base * __builtin_amdgcn_exp2f(sizeof(T) == 2 ? fmaf(v[j], LOG2E, -both) : fmaf(v[j], LOG2E, -m2) - l2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < CE; ++j) {
+          const float lp = v[j] - top - ls;
+          const float p = empty ? 0.0f : exp_of(lp);
+          v[j] = p * fmaf(-gh, fmaxf(lp, FAR), base);
+        }
       }
       if (tj >= j0 && tj < j0 + CE) {
 #pragma unroll
@@ -656,7 +671,8 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
         for (int j = 0; j < CE; ++j) v[j] = none || j0 + j >= V ? 0.0f : v[j];
       }
       if (whole) {
-        store_row<T, CE>(out + j0, v);
+        if (past) store_row_nt<T, CE>(out + j0, v);
+        else store_row<T, CE>(out + j0, v);
       } else {
 #pragma unroll
         for (int j = 0; j < CE; ++j)
@@ -732,7 +748,8 @@ hipError_t run_bwd(const void* z, const void* targets, bool wide, int M, int W, 
   const int chunks = W / (16 / (int)sizeof(T)) + 2, pieces = (chunks + BACK * TPR - 1) / (BACK * TPR);
   const size_t blocks = ((size_t)M * pieces + 256 / TPR - 1) / (256 / TPR);
   hipLaunchKernelGGL((logprobs_bwd_kernel<T, TPR>), dim3((unsigned)std::min<size_t>(blocks, 1 << 20)), dim3(256), 0, st,
-                     (const T*)z, targets, wide, M, W, V, ignore, pieces, stats, entropy, g_logp, g_lse, g_ent, (T*)gz);
+                     (const T*)z, targets, wide, M, W, V, ignore, pieces, stats, entropy, g_logp, g_lse, g_ent, (T*)gz,
+                     (size_t)M * W * sizeof(T) > CACHE);
   return hipGetLastError();
 }
 

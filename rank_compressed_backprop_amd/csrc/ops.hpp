@@ -329,11 +329,10 @@ hipError_t launch_logprobs_bwd(bool bf16_io, const void* z, const void* targets,
                                int64_t ignore, const float* stats, const float* entropy, const float* g_logp,
                                const float* g_lse, const float* g_ent, void* gz, hipStream_t st);
 
-// n tensors of count[i] elements, bf[i]: bfloat16, else float32 (all host arrays). factor: the
-// clipping factor is left at ws.
+// n tensors of count[i] elements, bf[i]: bfloat16, else float32 (all host arrays).
 size_t grad_norm_bytes(int n);
-hipError_t launch_grad_norm(const void* const* src, const int64_t* count, const int32_t* bf, int n, float max_norm,
-                            float* norm, void* ws, hipStream_t st, bool factor);
+hipError_t launch_grad_norm(const void* const* src, const int64_t* count, const int32_t* bf, int n, float* norm,
+                            void* ws, hipStream_t st);
 hipError_t launch_clip_grads(const void* const* src, const int64_t* count, const int32_t* bf, void* const* dst,
                              const int32_t* dst_bf, int n, float max_norm, float* norm, void* ws, hipStream_t st);
 

@@ -346,7 +346,7 @@ INSTANT_API instant_status instant_grad_norm(const void* const* grads, const int
   TRY(tensors(grads, count, dtype, n));
   if (!norm || off4(norm)) return INSTANT_E_ARG;
   TRY(workspace_ok(workspace, workspace_bytes, grad_norm_bytes(n)));
-  return hip_ok(launch_grad_norm(grads, count, dtype, n, 0.0f, norm, workspace, S(stream), false));
+  return hip_ok(launch_grad_norm(grads, count, dtype, n, norm, workspace, S(stream)));
 }
 
 INSTANT_API instant_status instant_clip_grads(const void* const* grads, const int64_t* count, const int32_t* dtype,

@@ -647,8 +647,9 @@ def token_logprobs(logits, targets=None, vocab=None, top=0, ignore=IGNORE) -> To
     if not 0 <= top <= min(MAX_TOP, V):
         raise ValueError(f"top must be 0 to {min(MAX_TOP, V)}, got {top}")
     _int64(ignore, "ignore")
-    logp = logits.new_empty(shape, dtype=torch.float32) if targets is not None else None
-    lse, entropy = (logits.new_empty(shape, dtype=torch.float32) for _ in range(2))
+    lse = logits.new_empty(shape, dtype=torch.float32)
+    entropy = torch.empty_like(lse)
+    logp = torch.empty_like(lse) if targets is not None else None
     stats = logits.new_empty((*shape, 2), dtype=torch.float32)
     tl = ti = None
     if top:
@@ -693,30 +694,32 @@ def token_logprobs_backward(logits, targets, stats, g_logp=None, g_lse=None, g_e
 # ----------------------------------------------------------------------------- gradients of a model
 
 def _grads(tensors, name):
-    """(tensors as a list, and of each the address, the elements and the dtype code)."""
+    """Of a sequence of tensors: the first, and of each the address, the elements and the dtype code."""
     if isinstance(tensors, Tensor):
         raise TypeError(f"{name} must be a sequence of tensors, got a tensor")
-    tensors = list(tensors)
-    if not tensors:
-        raise ValueError(f"{name} must hold a tensor at least")
     dev = torch.cuda.current_device() if torch.cuda.is_available() else None
     at, count, codes = [], [], []
     for t in tensors:
-        codes.append(_dtype(t, name))
+        code = _DTYPES.get(t.dtype) if isinstance(t, Tensor) else None
+        if code is None:
+            _dtype(t, name)
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+        codes.append(code)
         at.append(t.data_ptr())
         count.append(t.numel())
-    return tensors, at, count, codes
+    if not at:
+        raise ValueError(f"{name} must hold a tensor at least")
+    return tensors[0], at, count, codes
 
 
 def grad_norm(tensors) -> torch.Tensor:
     """The Euclidean norm over all elements of a sequence of tensors (float32 and bfloat16 in any
     mixture, of any shapes), a float32 scalar on the device. Squares are summed in float64."""
-    tensors, at, count, codes = _grads(tensors, "tensors")
-    n, first = len(tensors), tensors[0]
+    first, at, count, codes = _grads(list(tensors) if not isinstance(tensors, Tensor) else tensors, "tensors")
+    n = len(at)
     norm = first.new_empty((), dtype=torch.float32)
     size = _grads_bytes(n)
     ws, wp = _workspace(size, first)
@@ -728,21 +731,18 @@ def grad_norm(tensors) -> torch.Tensor:
 def clip_grads(tensors, max_norm, out=None) -> torch.Tensor:
     """Scales a sequence of tensors so that the norm over all their elements is at most max_norm:
     by max_norm / (norm + 1e-6) where that is below 1, else not at all. Returns the norm before (a
-    float32 scalar on the device; nothing waits for it). out: tensors of the same shapes, float32 or
-    bfloat16, that receive the result; None: the tensors themselves. Outputs may not share memory
+    float32 scalar on the device; nothing waits for it). out: as many tensors of as many elements each,
+    float32 or bfloat16, that receive the result; None: the tensors themselves. Outputs may not share memory
     with each other or with another tensor of the call."""
-    tensors, at, count, codes = _grads(tensors, "tensors")
+    first, at, count, codes = _grads(list(tensors) if not isinstance(tensors, Tensor) else tensors, "tensors")
     if not max_norm >= 0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
-    n, first = len(tensors), tensors[0]
+    n = len(at)
     to, to_codes = at, codes
     if out is not None:
-        out, to, _, to_codes = _grads(out, "out")
-        if len(out) != n:
-            raise ValueError(f"out must hold {n} tensors, got {len(out)}")
-        for t, o in zip(tensors, out):
-            if t.shape != o.shape:
-                raise ValueError(f"out must have the tensors' shapes, got {tuple(o.shape)} for {tuple(t.shape)}")
+        _, to, to_count, to_codes = _grads(list(out) if not isinstance(out, Tensor) else out, "out")
+        if to_count != count:
+            raise ValueError(f"out must hold tensors of {count} elements, got {to_count}")
     norm = first.new_empty((), dtype=torch.float32)
     size = _grads_bytes(n)
     ws, wp = _workspace(size, first)
