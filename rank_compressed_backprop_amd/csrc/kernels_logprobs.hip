@@ -165,8 +165,8 @@ template <int G> __device__ __forceinline__ int min_over(int v) {
   return over_lanes<G>(v, [](int a, int b) { return a < b ? a : b; });
 }
 
-// What the threads of a row have written to LDS is there for the others. (A plain barrier also waits
-// for stores to memory, microseconds while the chip streams: 130 of 330 us with alternatives.)
+// What the threads of a row have written to LDS is there for the others. (Stores to memory are not
+// waited for, as a plain barrier would.)
 template <int TPR> __device__ __forceinline__ void settled() {
 #ifdef __HIP_DEVICE_COMPILE__
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -259,8 +259,9 @@ __device__ __forceinline__ Target target_of(const T* row, const void* targets, b
 // cache), and the elements that reach it, a few more than k too, are ranked by counting.
 // Should more reach it than are held, the k-th of those held is a higher bound, and they are looked up
 // again (each time at least as many fewer reach it as are held, but k).
-// (16384 x 30522, k = 20: a row's tail is on the way of its block's next, so its instructions count:
-// reading all chunks of the threads whose best reaches the bound took 364 us.)
+// (16384 x 30522, k = 20, takes 310 us against 195 for k = 0 or 1: what follows a row's pass keeps its
+// block's registers from the next. Reading again all chunks of the threads whose best reaches the bound
+// took 364 us, holding such chunks in LDS during the pass 360.)
 template <class T, int TPR, int TOP, bool SPLIT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void logprobs_kernel(
     const T* __restrict__ z, const void* __restrict__ targets, bool wide, int M, int W, int V, int64_t ignore, int k,
@@ -269,9 +270,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void logprobs_kernel(
   constexpr int CE = R::CE, U = step_chunks(TPR, CE), RPB = TPR < 256 ? 256 / TPR : 1, WAVES = TPR < WAVE ? 1 : TPR / WAVE;
   constexpr int LANES = TPR < WAVE ? TPR : WAVE, CANDS = cands_of(TPR), PER = TPR / 64 ? TPR / 64 : 1;
   static_assert(TPR >= WAVE || TOP < 2, "ranking takes a wave");
-  // few rows: a block goes through its code once or twice, and most of its time is the code's way from
-  // memory, so every chunk takes the same short loop (64 x 128000: 14 us, with steps of U chunks 18)
-  constexpr bool SMALL = TPR == 1024;
+  // Every chunk by the same short loop, not a step of U at a time. Few rows: a block goes through its code
+  // once or twice, and much of its time is the code's way from memory (64 x 128000 in float32: 14 us a
+  // slice kernel, with steps 18). Short rows with alternatives: fewer registers, so more rows at a time
+  // (16384 x 1000, k = 5: 33 -> 28 us; 16384 x 30522 gains nothing, and 8192 x 128000 loses a fifth).
+  constexpr bool SMALL = TPR == 1024 || (TPR == WAVE && TOP == 2);
   __shared__ float sums[RPB][3][WAVES];
   __shared__ uint64_t groups_[TOP == 2 ? RPB : 1][64], cand_[TOP == 2 ? RPB : 1][TOP == 2 ? CANDS + PAD : 1];
   __shared__ uint64_t bound_[RPB];

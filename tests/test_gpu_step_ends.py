@@ -4,13 +4,14 @@ log probabilities, gradient norm and clipping, against plain 64-bit implementati
 Tolerances. u = 2^-24 and U (bf16 2^-8, fp32 2^-24) are half a step relative to the value: what one
 rounding is off by at most.
 
-Log probabilities. With t = z - m <= 0 an exponential is taken of a float32 t times a float32
-log2(e): three roundings that reach it |t|-fold, and the hardware's own 1 ulp, so a term of S is off
-by at most (3 |t| + 2) u of itself. |t| is at most D, the row's range (104 at most: below, the term
-is 0 in float32, which is off by less than V 2^-149). A running sum of n terms of one sign adds n u,
-and each of its n / 32 + 12 raises of the maximum (the joins of threads among them) multiplies by an
-exponential of its own (4 u and 3 u times the distance, D in all): REL(n, D) below, with n = V the
-most that one thread may hold. E has terms of one sign too and the same bound, relative to itself.
+Log probabilities. With t = z - m <= 0 an exponential is taken of log2(e) t, evaluated in float32: at
+most three roundings (the difference, log2(e), the product) that reach it |t|-fold, and the hardware's
+own 1 ulp, so a term of S is off by at most (3 |t| + 2) u of itself. |t| is at most D, the row's range
+(104 at most: below, the term is 0 in float32, which is off by less than V 2^-149). A running sum of n
+terms of one sign adds n u, and each of its n / 32 + 12 raises of the maximum (the joins of threads
+among them) multiplies by an exponential of its own (4 u and 3 u times the distance, D in all):
+REL(n, D) below, with n = V the most that one thread may hold. E has terms of one sign too and the same
+bound, relative to itself.
 """
 import zlib
 
