@@ -14,6 +14,7 @@ on its current stream. None of them is differentiable by itself: ``linear.py``, 
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import math
@@ -165,9 +166,18 @@ def instant_logprobs_bwd(logits, targets, token_bytes, M, W, V, dtype, ignore, s
                                      _stream(stream))
 
 
-def _host(kind, values):
-    """A host array of the call (NULL for None)."""
-    return None if values is None else (kind * len(values))(*values)
+class _Host:
+    """A host array of the call ('Q' addresses, 'q' int64, 'i' int32) and its address (NULL for None). The
+    caller keeps it until the call returns."""
+    __slots__ = ("held", "at")
+
+    def __init__(self, code, values):
+        self.held = None if values is None else array.array(code, values)
+        self.at = None if values is None else self.held.buffer_info()[0]
+
+
+def _addresses(tensors):
+    return None if tensors is None else [_ptr(t) or 0 for t in tensors]
 
 
 def instant_grad_norm_workspace_bytes(n) -> int:
@@ -176,17 +186,17 @@ def instant_grad_norm_workspace_bytes(n) -> int:
 
 def instant_grad_norm(grads, count, dtype, n, norm, workspace, workspace_bytes, stream=None) -> int:
     """grads (tensors or addresses), count and dtype are sequences of n."""
-    return _lib.instant_grad_norm(_host(_vp, None if grads is None else [_ptr(g) for g in grads]), _host(_l, count),
-                                  _host(_i, dtype), n, _ptr(norm), _ptr(workspace), workspace_bytes, _stream(stream))
+    g, c, d = _Host("Q", _addresses(grads)), _Host("q", count), _Host("i", dtype)
+    return _lib.instant_grad_norm(g.at, c.at, d.at, n, _ptr(norm), _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def instant_clip_grads(grads, count, dtype, out, out_dtype, n, max_norm, norm, workspace, workspace_bytes,
                        stream=None) -> int:
     """grads, count, dtype, out and out_dtype are sequences of n."""
-    g, o = (None if t is None else [_ptr(x) for x in t] for t in (grads, out))
-    return _lib.instant_clip_grads(_host(_vp, g), _host(_l, count), _host(_i, dtype), _host(_vp, o),
-                                   _host(_i, out_dtype), n, max_norm, _ptr(norm), _ptr(workspace), workspace_bytes,
-                                   _stream(stream))
+    g, c, d = _Host("Q", _addresses(grads)), _Host("q", count), _Host("i", dtype)
+    o, e = _Host("Q", _addresses(out)), _Host("i", out_dtype)
+    return _lib.instant_clip_grads(g.at, c.at, d.at, o.at, e.at, n, max_norm, _ptr(norm), _ptr(workspace),
+                                   workspace_bytes, _stream(stream))
 
 
 # ----------------------------------------------------------------------------- checks
@@ -694,37 +704,38 @@ def token_logprobs_backward(logits, targets, stats, g_logp=None, g_lse=None, g_e
 # ----------------------------------------------------------------------------- gradients of a model
 
 def _grads(tensors, name):
-    """Of a sequence of tensors: the first, and of each the address, the elements and the dtype code."""
+    """Of a sequence of tensors: the first, and of each the address, the elements and the dtype code (a
+    model has hundreds: each question is put to all of them at once)."""
     if isinstance(tensors, Tensor):
         raise TypeError(f"{name} must be a sequence of tensors, got a tensor")
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    at, count, codes = [], [], []
-    for t in tensors:
-        code = _DTYPES.get(t.dtype) if isinstance(t, Tensor) else None
-        if code is None:
-            _dtype(t, name)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        codes.append(code)
-        at.append(t.data_ptr())
-        count.append(t.numel())
-    if not at:
+    tensors = list(tensors)
+    if not tensors:
         raise ValueError(f"{name} must hold a tensor at least")
-    return tensors[0], at, count, codes
+    try:
+        codes = [_DTYPES[t.dtype] for t in tensors]
+        devices = set(map(Tensor.get_device, tensors))
+    except (KeyError, AttributeError, TypeError):
+        for t in tensors:  # says which it is
+            _dtype(t, name)
+        raise
+    if devices != {torch.cuda.current_device() if torch.cuda.is_available() else None}:
+        raise ValueError(f"{name} must be on the current CUDA device, got {[str(t.device) for t in tensors]}")
+    if not all(map(Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    return tensors[0], list(map(Tensor.data_ptr, tensors)), list(map(Tensor.numel, tensors)), codes
 
 
 def grad_norm(tensors) -> torch.Tensor:
     """The Euclidean norm over all elements of a sequence of tensors (float32 and bfloat16 in any
     mixture, of any shapes), a float32 scalar on the device. Squares are summed in float64."""
-    first, at, count, codes = _grads(list(tensors) if not isinstance(tensors, Tensor) else tensors, "tensors")
+    first, at, count, codes = _grads(tensors, "tensors")
     n = len(at)
     norm = first.new_empty((), dtype=torch.float32)
     size = _grads_bytes(n)
     ws, wp = _workspace(size, first)
-    _ok(_lib.instant_grad_norm(_host(_vp, at), _host(_l, count), _host(_i, codes), n, norm.data_ptr(), wp, size,
-                               _current(first.get_device())), "instant_grad_norm")
+    g, c, d = _Host("Q", at), _Host("q", count), _Host("i", codes)
+    _ok(_lib.instant_grad_norm(g.at, c.at, d.at, n, norm.data_ptr(), wp, size, _current(first.get_device())),
+        "instant_grad_norm")
     return norm
 
 
@@ -734,19 +745,19 @@ def clip_grads(tensors, max_norm, out=None) -> torch.Tensor:
     float32 scalar on the device; nothing waits for it). out: as many tensors of as many elements each,
     float32 or bfloat16, that receive the result; None: the tensors themselves. Outputs may not share memory
     with each other or with another tensor of the call."""
-    first, at, count, codes = _grads(list(tensors) if not isinstance(tensors, Tensor) else tensors, "tensors")
+    first, at, count, codes = _grads(tensors, "tensors")
     if not max_norm >= 0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
     n = len(at)
     to, to_codes = at, codes
     if out is not None:
-        _, to, to_count, to_codes = _grads(list(out) if not isinstance(out, Tensor) else out, "out")
+        _, to, to_count, to_codes = _grads(out, "out")
         if to_count != count:
             raise ValueError(f"out must hold tensors of {count} elements, got {to_count}")
     norm = first.new_empty((), dtype=torch.float32)
     size = _grads_bytes(n)
     ws, wp = _workspace(size, first)
-    _ok(_lib.instant_clip_grads(_host(_vp, at), _host(_l, count), _host(_i, codes), _host(_vp, to), _host(_i, to_codes),
-                                n, max_norm, norm.data_ptr(), wp, size, _current(first.get_device())),
-        "instant_clip_grads")
+    g, c, d, o, e = _Host("Q", at), _Host("q", count), _Host("i", codes), _Host("Q", to), _Host("i", to_codes)
+    _ok(_lib.instant_clip_grads(g.at, c.at, d.at, o.at, e.at, n, max_norm, norm.data_ptr(), wp, size,
+                                _current(first.get_device())), "instant_clip_grads")
     return norm
