@@ -358,8 +358,8 @@ template <class T>
 __global__ __launch_bounds__(SUM_WAVES* WAVE) void run_sum_kernel(const T* __restrict__ gy, Grouped grouped, int C,
                                                                   float scale, bool add, T* __restrict__ gw,
                                                                   float* __restrict__ part) {
-  __shared__ __attribute__((aligned(32))) float ends[2][SUM_WAVES][8 * WAVE];  // of each wave: its first run's sum if that began before, and its
-                                                  // last run's if that begins here and goes on
+  // of each wave: its first run's sum if that began before, and its last run's if that begins here and goes on
+  __shared__ __attribute__((aligned(32))) float ends[2][SUM_WAVES][8 * WAVE];
   const int M = *grouped.used, tile = blockIdx.x, i0 = tile * TILE;
   if (i0 >= M) return;
   const int count = min(TILE, M - i0), lane = threadIdx.x % WAVE, col = 8 * (WAVE * blockIdx.y + lane);

@@ -635,12 +635,11 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
     const bool empty = ls == -INFINITY;                         // p = 0
     const float base = gl - g - (gh != 0.0f ? gh * entropy[row] : 0.0f);
     const int tj = t >= 0 && t < V ? (int)t : -1;
-    // Without an entropy gradient a value is p * base, with p's exponent of two in two operations, or one
-    // for a bfloat16 result: fl(log2(e) (top + ls)) is off by 2^-24 of itself, and p by 2^-19 of itself
-    // where that is 30, against 2^-9 of the result's own rounding. (16384 x 30522 392 -> 387 us: bound by
-    // memory either way.)
+    // Without an entropy gradient a value is p * base, with p's exponent of two in two operations. (Not in
+    // one: log2(e) (top + ls) as one float32 is off by 2^-24 of itself, which for a top of 10^5 is more
+    // than a bfloat16 result's own rounding.)
     const bool plain = gh == 0.0f && !empty && near(top);
-    const float m2 = top * LOG2E, l2 = fmaf(ls, LOG2E, rest(top)), both = m2 + l2;
+    const float m2 = top * LOG2E, l2 = fmaf(ls, LOG2E, rest(top));
 #pragma unroll
     for (int b = 0; b < BACK; ++b) {
       const int c = c0 + b * TPR, j0 = r.first(c);
@@ -655,8 +654,7 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
       }
       if (plain) {
 #pragma unroll
-        for (int j = 0; j < CE; ++j)
-          v[j] = base * __builtin_amdgcn_exp2f(sizeof(T) == 2 ? fmaf(v[j], LOG2E, -both) : fmaf(v[j], LOG2E, -m2) - l2);
+        for (int j = 0; j < CE; ++j) v[j] = base * __builtin_amdgcn_exp2f(fmaf(v[j], LOG2E, -m2) - l2);
       } else {
 #pragma unroll
         for (int j = 0; j < CE; ++j) {

@@ -211,6 +211,12 @@ bool logits_ok(const void* z, int32_t dtype) { return ((uintptr_t)z) % (dtype ==
 
 template <class... P> bool off4(P... p) { return (... || (((uintptr_t)p) % 4)); }
 
+// whether [a, a + na) and [b, b + nb), in elements of dtype, share memory
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb, int32_t dtype) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b, e = dtype == INSTANT_BF16 ? 2 : 4;
+  return x < y + (uintptr_t)nb * e && y < x + (uintptr_t)na * e;
+}
+
 instant_status embed_sizes(int32_t M, int32_t V, int32_t C) {
   TRY(sizes(M, {C}));
   if (V < 1) return INSTANT_E_ARG;
@@ -289,7 +295,7 @@ INSTANT_API instant_status instant_embed_bwd(const void* gy, const void* tokens,
   if (!dtype_ok(dtype) || !tokens_ok(tokens, token_bytes) || off16(gy, gtable) || !std::isfinite(scale) || !gtable ||
       padding < -1)
     return INSTANT_E_ARG;
-  if (M > 0 && (!gy || !tokens)) return INSTANT_E_ARG;
+  if (M > 0 && (!gy || !tokens || overlap(gy, (int64_t)M * C, gtable, (int64_t)V * C, dtype))) return INSTANT_E_ARG;
   TRY(workspace_ok(workspace, workspace_bytes, embed_bwd_bytes(M, C)));
   return hip_ok(launch_embed_bwd(dtype == INSTANT_BF16, gy, tokens, token_bytes == 8, M, V, C, scale, padding,
                                  accumulate != 0, gtable, workspace, S(stream)));
@@ -332,6 +338,7 @@ INSTANT_API instant_status instant_logprobs_bwd(const void* logits, const void* 
   if (M == 0) return INSTANT_OK;
   if (!logits || !stats || !gz || (!g_logp && !g_lse && !g_entropy)) return INSTANT_E_ARG;
   if ((g_logp && !targets) || (g_entropy && !entropy)) return INSTANT_E_ARG;
+  if (gz != logits && overlap(gz, (int64_t)M * W, logits, (int64_t)M * W, dtype)) return INSTANT_E_ARG;
   return hip_ok(launch_logprobs_bwd(dtype == INSTANT_BF16, logits, targets, token_bytes == 8, M, W, V, ignore, stats,
                                     entropy, g_logp, g_lse, g_entropy, gz, S(stream)));
 }

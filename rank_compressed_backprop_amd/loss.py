@@ -14,9 +14,8 @@ class _TokenLogprobsFn(torch.autograd.Function):
         ctx.save_for_backward(logits, targets, out.stats, out.entropy)
         ctx.vocab, ctx.ignore = vocab, ignore
         ctx.set_materialize_grads(False)
-        if top:
-            ctx.mark_non_differentiable(out.top_logp, out.top_index)
-        ctx.mark_non_differentiable(out.stats)
+        # (in one call: each replaces the one before)
+        ctx.mark_non_differentiable(out.stats, *((out.top_logp, out.top_index) if top else ()))
         return tuple(out)
 
     @staticmethod

@@ -280,6 +280,28 @@ def test_logprobs_largest_magnitudes_and_tails(dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("v", [40, 1000, 5003])
+def test_gradient_of_large_equal_logits(v, dtype):
+    """Two equal logits, far above all others: p is 1/2 whatever they are, so the gradient is half of
+    what comes in. The exponents of the two are rests of roundings, exact, and sums of magnitude 1: 16 u
+    hold them, log S and both exponentials (2 u each) in forward and backward pass."""
+    from rank_compressed_backprop_amd import ops
+    tops = [100.0, 1000.0, 4096.0, 12345.0, 65536.0, 100000.0, 523000.0, 1048576.0, 3e6, 1e9, -1000.0, -70000.0]
+    z = torch.full((len(tops), v), -INF, dtype=dtype)
+    z[:, 3] = z[:, v - 2] = torch.tensor(tops).to(dtype)
+    z[:, 7] = z[:, 3] * torch.tensor([0.5 if x > 0 else 2.0 for x in tops])
+    z, t = z.cuda(), torch.full((len(tops),), 3).cuda()
+    g = randn(gen("equal", v), len(tops))
+    out = ops.token_logprobs(z, t)
+    within("logp", out.logp, torch.full((len(tops),), 0.5, dtype=torch.float64).log().cuda(), 16 * u)
+    for gl, p_of in ((None, -0.5), (g.clone(), 0.0)):
+        gz = ops.token_logprobs_backward(z, t, out.stats, g, gl).double()
+        want = torch.zeros_like(gz)
+        want[:, v - 2], want[:, 3] = g.double() * p_of, g.double() * (1 + p_of)
+        within("gz", gz, want, U[dtype] * want.abs() * (1 + 2.0 ** -20) + 32 * u * g.abs().double()[:, None])
+
+
+@DTYPES
 @pytest.mark.parametrize("m,v", [(5, 57), (33, 1001), (3, 40007)])
 def test_gradient_in_place_and_inside(m, v, dtype):
     """Outputs at odd places stay inside their rows; in place gives the same bits."""
@@ -691,6 +713,19 @@ def test_layers_refuse_second_derivatives_and_bad_arguments():
         with pytest.raises(InstantError):  # outputs that share memory
             ops.clip_grads(ts, 1.0, out)
     assert ops.grad_norm([y, y]) == 0
+    w = torch.zeros(16, 8, device="cuda")
+    with pytest.raises(InstantError):  # a gradient that is added to itself
+        ops.embedding_backward(w, torch.arange(16).cuda(), 16, into=w)
+
+
+def test_alternatives_take_no_gradient():
+    from rank_compressed_backprop_amd.loss import token_logprobs
+    z = torch.randn(4, 16, device="cuda", requires_grad=True)
+    out = token_logprobs(z, torch.arange(4).cuda(), top=3)
+    assert out.logp.requires_grad and out.lse.requires_grad and out.entropy.requires_grad
+    assert not (out.top_logp.requires_grad or out.top_index.requires_grad or out.stats.requires_grad)
+    with pytest.raises(RuntimeError):
+        out.top_logp.sum().backward()
 
 
 @pytest.mark.parametrize("tied", [False, True])

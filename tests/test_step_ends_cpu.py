@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 import rank_compressed_backprop_amd as rcb  # noqa: E402
 from rank_compressed_backprop_amd import ops  # noqa: E402
 
-A, W = 0x1000, 0x2000  # pointers that are never read: every call here is refused, or has no rows
+A, W, FAR = 0x1000, 0x2000, 1 << 44  # pointers that are never read: every call here is refused, or has no rows
 E_ARG, E_SHAPE, OK = rcb.INSTANT_E_ARG, rcb.INSTANT_E_SHAPE, rcb.INSTANT_OK
 BF, FP = rcb.INSTANT_BF16, rcb.INSTANT_FP32
 INF, NAN = float("inf"), float("nan")
@@ -19,7 +19,7 @@ def embed_fwd(tokens=A, size=8, M=4, table=A, V=50, C=64, dtype=BF, scale=1.0, y
     return ops.instant_embed_fwd(tokens, size, M, table, V, C, dtype, scale, y, 0)
 
 
-def embed_bwd(gy=A, tokens=A, size=8, M=4, V=50, C=64, dtype=BF, scale=1.0, padding=-1, add=0, gt=A, ws=W, n=1 << 40):
+def embed_bwd(gy=A, tokens=A, size=8, M=4, V=50, C=64, dtype=BF, scale=1.0, padding=-1, add=0, gt=FAR, ws=W, n=1 << 40):
     return ops.instant_embed_bwd(gy, tokens, size, M, V, C, dtype, scale, padding, add, gt, ws, n, 0)
 
 
@@ -32,7 +32,7 @@ def test_embed_refusals():
         assert embed_fwd(**change) == E_SHAPE, change
     assert embed_fwd(M=0, tokens=None, table=None, y=None) == OK
     for change in [dict(gy=None), dict(tokens=None), dict(gt=None), dict(size=3), dict(tokens=A + 1), dict(gy=A + 2),
-                   dict(gt=A + 8), dict(M=-1), dict(V=0), dict(C=-8), dict(dtype=9), dict(scale=INF), dict(padding=-2),
+                   dict(gt=FAR + 8), dict(gt=A), dict(gt=A + 496), dict(gy=FAR + 6384), dict(M=-1), dict(V=0), dict(C=-8), dict(dtype=9), dict(scale=INF), dict(padding=-2),
                    dict(ws=None), dict(ws=W + 64)]:
         assert embed_bwd(**change) == E_ARG, change
     for change in [dict(C=20), dict(M=(1 << 22) + 1), dict(M=1 << 22, C=1 << 17), dict(V=(1 << 18) + 8), dict(n=16)]:
