@@ -195,8 +195,9 @@ template <int TPR, class F> __device__ __forceinline__ void ranked(const uint64_
   }
 }
 
-// Chunks of a step (1024 threads have 128 registers each).
-constexpr int step_chunks(int tpr, int ce) { return (tpr == 1024 ? 16 : 32) / ce; }
+// Chunks of a step (1024 threads have 128 registers each; a wave with alternatives takes as few, so that four
+// blocks fit a compute unit).
+constexpr int step_chunks(int tpr, int ce, int top) { return (tpr == 1024 || (tpr == WAVE && top == 2) ? 16 : 32) / ce; }
 // Alternatives that are held for ranking, for a row of a wave or of a block.
 constexpr int cands_of(int tpr) { return tpr == 64 ? 512 : 1024; }
 constexpr int MAX_SLICES = 16, JOIN_KEYS = 512;  // of a row, and their alternatives
@@ -259,22 +260,22 @@ __device__ __forceinline__ Target target_of(const T* row, const void* targets, b
 // cache), and the elements that reach it, a few more than k too, are ranked by counting.
 // Should more reach it than are held, the k-th of those held is a higher bound, and they are looked up
 // again (each time at least as many fewer reach it as are held, but k).
-// (16384 x 30522, k = 20, takes 310 us against 195 for k = 0 or 1: what follows a row's pass keeps its
-// block's registers from the next. Reading again all chunks of the threads whose best reaches the bound
-// took 364 us, holding such chunks in LDS during the pass 360.)
+// (16384 x 30522, k = 20, takes 251 us against 195 for k = 0 or 1, back to back: what follows a row's pass
+// keeps its registers from the next row. A block of 256 threads a row, with its barriers, took 310;
+// reading again all chunks of the threads whose best reaches the bound 364, holding such chunks in LDS
+// during the pass 360.)
 template <class T, int TPR, int TOP, bool SPLIT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void logprobs_kernel(
     const T* __restrict__ z, const void* __restrict__ targets, bool wide, int M, int W, int V, int64_t ignore, int k,
     Out out, int slices, float* __restrict__ parts, uint64_t* __restrict__ keys, int most_steps) {
   typedef Row<T> R;
-  constexpr int CE = R::CE, U = step_chunks(TPR, CE), RPB = TPR < 256 ? 256 / TPR : 1, WAVES = TPR < WAVE ? 1 : TPR / WAVE;
+  constexpr int CE = R::CE, U = step_chunks(TPR, CE, TOP), RPB = TPR < 256 ? 256 / TPR : 1, WAVES = TPR < WAVE ? 1 : TPR / WAVE;
   constexpr int LANES = TPR < WAVE ? TPR : WAVE, CANDS = cands_of(TPR), PER = TPR / 64 ? TPR / 64 : 1;
   static_assert(TPR >= WAVE || TOP < 2, "ranking takes a wave");
   // Every chunk by the same short loop, not a step of U at a time. Few rows: a block goes through its code
-  // once or twice, and much of its time is the code's way from memory (64 x 128000 in float32: 14 us a
-  // slice kernel, with steps 18). Short rows with alternatives: fewer registers, so more rows at a time
-  // (16384 x 1000, k = 5: 33 -> 28 us; 16384 x 30522 gains nothing, and 8192 x 128000 loses a fifth).
-  constexpr bool SMALL = TPR == 1024 || (TPR == WAVE && TOP == 2);
+  // once or twice, and much of its time is the code's way from memory. (64 x 128000 in float32: 14 us a
+  // slice kernel, with steps 18.) For many rows it is slower (8192 x 128000, k = 20: 425 -> 546 us).
+  constexpr bool SMALL = TPR == 1024;
   __shared__ float sums[RPB][3][WAVES];
   __shared__ uint64_t groups_[TOP == 2 ? RPB : 1][64], cand_[TOP == 2 ? RPB : 1][TOP == 2 ? CANDS + PAD : 1];
   __shared__ uint64_t bound_[RPB];
@@ -706,12 +707,12 @@ struct Call {
 };
 
 // Steps of a row of `chunks` chunks at most (logprobs_kernel, TOP 2), and their bytes of LDS a block.
-template <class T, int TPR> int most_steps(int chunks) { return chunks / (step_chunks(TPR, 16 / sizeof(T)) * TPR) + 1; }
+template <class T, int TPR, int TOP> int most_steps(int chunks) { return chunks / (step_chunks(TPR, 16 / sizeof(T), TOP) * TPR) + 1; }
 template <int TPR, int TOP> size_t lds_bytes(int steps) { return TOP == 2 ? (size_t)steps * std::max(TPR, 256) * 2 : 0; }
 
 template <class T, int TPR, int TOP> hipError_t run_fwd(const Call& c) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-  const int steps = most_steps<T, TPR>(c.V / (16 / (int)sizeof(T)) + 2);
+  const int steps = most_steps<T, TPR, TOP>(c.V / (16 / (int)sizeof(T)) + 2);
   hipLaunchKernelGGL((logprobs_kernel<T, TPR, TOP, false>), dim3(std::min((c.M + RPB - 1) / RPB, 1 << 20)),
                      dim3(TPR < 256 ? 256 : TPR), (lds_bytes<TPR, TOP>(steps)), c.st, (const T*)c.z, c.targets, c.wide,
                      c.M, c.W, c.V, c.ignore, c.k, c.out, 1, nullptr, nullptr, steps);
@@ -723,7 +724,7 @@ template <class T, int TOP> hipError_t run_top(const Call& c, void* ws) {
   if (slices > 1) {
     uint64_t* keys = (uint64_t*)ws;
     float* parts = (float*)(keys + (size_t)c.M * slices * c.k);
-    const int steps = most_steps<T, 1024>((chunks + 2) / slices + 1);
+    const int steps = most_steps<T, 1024, TOP>((chunks + 2) / slices + 1);
     hipLaunchKernelGGL((logprobs_kernel<T, 1024, TOP, true>), dim3(c.M * slices), dim3(1024), (lds_bytes<1024, TOP>(steps)),
                        c.st, (const T*)c.z, c.targets, c.wide, c.M, c.W, c.V, c.ignore, c.k, c.out, slices, parts, keys,
                        steps);
@@ -733,7 +734,10 @@ template <class T, int TOP> hipError_t run_top(const Call& c, void* ws) {
   }
   if constexpr (TOP < 2)
     if (chunks <= 128) return run_fwd<T, 16, TOP>(c);
-  if (chunks <= 512) return run_fwd<T, 64, TOP>(c);
+  // A wave a row has no barriers, a block a row fewer rows at a time. (Calls, 256 threads and a wave: 16384 x
+  // 8000 in bfloat16 66 and 51 us, with k = 5 127 and 71; 16384 x 16000 95 and 97, 156 and 118; 4096 x 30522
+  // 51 and 50, 74 and 61; 4096 x 64000 91 and 94, 104 and 130. With 1024 rows of 30522 14 and 16, 23 and 26.)
+  if (chunks <= (c.M < 2048 ? 512 : TOP == 2 ? 4096 : 1024)) return run_fwd<T, 64, TOP>(c);
   if (chunks < 1024 || c.M > 256) return run_fwd<T, 256, TOP>(c);
   return run_fwd<T, 1024, TOP>(c);
 }

@@ -163,7 +163,8 @@ def check_backward(z, t, out, g, gl, gh, vocab=None, ignore=-100, in_place=False
 
 LOGIT_SHAPES = [(1, 1, 0), (1, 2, 1), (3, 7, 7), (5, 33, 32), (2, 255, 5), (4, 256, 32), (7, 257, 3), (3, 1001, 20),
                 (2, 2047, 32), (2, 2048, 32), (3, 2056, 32), (3, 2065, 31), (2, 4099, 1), (3, 30522, 20), (2, 32000, 5),
-                (1, 32768, 32), (1, 40001, 32), (300, 16387, 2), (1, 131071, 32), (1, 262144, 32), (65, 2500, 0)]
+                (1, 32768, 32), (1, 40001, 32), (300, 16387, 2), (1, 131071, 32), (1, 262144, 32), (65, 2500, 0),
+                (2048, 8000, 0), (2050, 8199, 1), (2049, 4099, 32), (2051, 9001, 5), (2048, 16391, 20), (2048, 32771, 2)]
 
 
 @DTYPES
@@ -203,6 +204,19 @@ def test_masked_and_strange_rows(v, dtype):
     """-inf, the type's lowest, whole rows of either, one value left, equal rows, infinities, NaN."""
     print(f"[masked] {v} {dtype}", flush=True)
     g = gen("mask", v)
+    z, t = strange_rows(g, v, dtype)
+    rows = len(t)
+    out = check_forward(z, t, 32 if v >= 32 else v)
+    assert out.lse[1] == -INF and out.entropy[1] == 0 and out.logp[1] == -INF
+    assert out.logp[9] == -INF and out.logp[10] == 0 and out.logp[11] == 0
+    assert out.lse[7].isnan() and out.logp[8].isnan() and out.entropy[7].isnan()
+    gz = check_backward(z, t, out, randn(g, rows), None, randn(g, rows))
+    assert gz[7].isnan().all() and not gz[1][t[1]].isnan()
+    gz = check_backward(z, t, out, randn(g, rows), None, None)
+    assert not gz[10].any() and not gz[11].any()  # padding: zeros, whatever the row holds
+
+
+def strange_rows(g, v, dtype):
     low = torch.finfo(dtype).min
     rows = 14
     z = randn(g, rows, v, dtype=dtype, sd=2.0)
@@ -228,14 +242,7 @@ def test_masked_and_strange_rows(v, dtype):
     z[12] = low
     z[12, v - 2] = torch.finfo(dtype).max / 2   # differences beyond float's range
     z[13] = torch.finfo(dtype).max
-    out = check_forward(z, t, 32 if v >= 32 else v)
-    assert out.lse[1] == -INF and out.entropy[1] == 0 and out.logp[1] == -INF
-    assert out.logp[9] == -INF and out.logp[10] == 0 and out.logp[11] == 0
-    assert out.lse[7].isnan() and out.logp[8].isnan() and out.entropy[7].isnan()
-    gz = check_backward(z, t, out, randn(g, rows), None, randn(g, rows))
-    assert gz[7].isnan().all() and not gz[1][t[1]].isnan()
-    gz = check_backward(z, t, out, randn(g, rows), None, None)
-    assert not gz[10].any() and not gz[11].any()  # padding: zeros, whatever the row holds
+    return z, t
 
 
 @DTYPES
@@ -245,7 +252,27 @@ def test_alternatives_in_hard_orders(v, k, dtype):
     """Rows in order, steps of equal values, and many values that beat the rest in the places of a
     few threads (more than the kernel holds at a time)."""
     print(f"[order] {v} {k} {dtype}", flush=True)
-    g = gen("order", v, k)
+    z = hard_rows(gen("order", v, k), v, dtype)
+    check_forward(z, torch.arange(7).cuda(), k)
+    one = z[4:5].contiguous()         # (few rows: other blocks)
+    check_forward(one, torch.zeros(1, dtype=torch.int64, device="cuda"), k)
+
+
+@DTYPES
+@pytest.mark.parametrize("v", [1000, 8191, 15997, 32700])
+@pytest.mark.parametrize("k", [1, 5, 32])
+def test_many_hard_and_strange_rows(v, k, dtype):
+    """The rows of the two tests before this among two thousand (other kernels take those)."""
+    print(f"[many] {v} {k} {dtype}", flush=True)
+    g = gen("many", v, k)
+    z, t = strange_rows(g, v, dtype)
+    z = torch.cat((z, hard_rows(g, v, dtype)))
+    t = torch.cat((t, torch.arange(7).cuda()))
+    times = 2058 // len(t)
+    check_forward(z.repeat(times, 1), t.repeat(times), k)
+
+
+def hard_rows(g, v, dtype):
     z = torch.zeros(7, v)
     ramp = torch.linspace(-20, 20, v)
     z[0], z[1] = ramp, ramp.flip(0)
@@ -257,10 +284,7 @@ def test_alternatives_in_hard_orders(v, k, dtype):
     z[5] = -30
     z[5, v // 2:v // 2 + 2000] = 3.0
     z[6] = torch.randint(0, 3, (v,), generator=g)
-    z = z.to(dtype).cuda()
-    check_forward(z, torch.arange(7).cuda(), k)
-    one = z[4:5].contiguous()         # (few rows: other blocks)
-    check_forward(one, torch.zeros(1, dtype=torch.int64, device="cuda"), k)
+    return z.to(dtype).cuda()
 
 
 @DTYPES
