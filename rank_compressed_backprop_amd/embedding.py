@@ -25,10 +25,12 @@ class InstantEmbedding(torch.nn.Module):
     """Rows of weight [V, C] looked up by token (int64 or int32, any shape) and multiplied by scale
     (sqrt(C) in many language models); V <= 2^18, C a multiple of 8, dtype "bf16" or "fp32".
 
-    padding: a token whose row gets no gradient (its row is zeros at the start). The weight may also
-    be the last product's (tied): hand it to both, autograd adds the gradients. The gradient is
-    dense [V, C], has the same bits every time, and cannot be differentiated again
-    (create_graph=True raises RuntimeError)."""
+    padding: a token whose row gets no gradient through the lookup (zeros at the start, unless the
+    weight is given). weight: where the weight starts. A Parameter of the layer's type and device,
+    contiguous, is taken as it is, so it may also be the last product's (tied): hand one Parameter,
+    or one layer's weight, to both constructors, and autograd adds the gradients. Anything else is
+    copied, and not tied. The gradient is dense [V, C], has the same bits every time, and cannot be
+    differentiated again (create_graph=True raises RuntimeError)."""
 
     def __init__(self, V, C, scale=1.0, padding=None, dtype="bf16", weight=None, device="cuda"):
         super().__init__()
@@ -41,14 +43,16 @@ class InstantEmbedding(torch.nn.Module):
         if padding is not None and not 0 <= padding < V:
             raise ValueError(f"padding must be a token of the vocabulary, got {padding}")
         self.V, self.C, self.scale, self.padding = int(V), int(C), float(scale), padding
+        torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         if weight is None:
             weight = torch.randn(self.V, self.C, device=device) * self.C ** -0.5
             if padding is not None:
                 weight[padding] = 0
+            self.weight = torch.nn.Parameter(weight.to(torch_dtype))
         elif tuple(weight.shape) != (self.V, self.C):
             raise ValueError(f"weight must be [{V}, {C}], got {tuple(weight.shape)}")
-        self.weight = torch.nn.Parameter(weight.to(device=device, dtype=torch.bfloat16 if dtype == "bf16"
-                                                   else torch.float32).contiguous())
+        else:
+            self.weight = ops.weight_parameter(weight, device, torch_dtype)
 
     def forward(self, tokens):
         return _EmbeddingFn.apply(tokens.contiguous(), self.weight, self.scale, self.padding)

@@ -126,6 +126,9 @@ class InstantLinear(torch.nn.Module):
     activation's slope). A norm that writes its output in 8 bits (norm.InstantRMSNorm) hands
     that over as x8, and nothing is packed here. The low-rank steps keep x_hat as ever.
 
+    weight: where the weight starts. A Parameter of the layer's type and device, contiguous, is taken
+    as it is, so one that other layers hold too (an embedding's, say) is tied; anything else is copied.
+
     The library's backward passes cannot be differentiated again: with any of these options a
     backward pass with create_graph=True raises RuntimeError.
 
@@ -154,8 +157,9 @@ class InstantLinear(torch.nn.Module):
         self.N_t, self.N_cal = int(N_t), int(N_cal)
         self.torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         if weight is None:
-            weight = torch.randn(Cy, Cx, device=device) / math.sqrt(Cx)
-        self.weight = torch.nn.Parameter(weight.to(device=device, dtype=self.torch_dtype).contiguous())
+            self.weight = torch.nn.Parameter((torch.randn(Cy, Cx, device=device) / math.sqrt(Cx)).to(self.torch_dtype))
+        else:
+            self.weight = ops.weight_parameter(weight, device, self.torch_dtype)
         self.activation, self.checkpoint = activation, checkpoint
         self.bias = torch.nn.Parameter(torch.zeros(Cy, dtype=self.torch_dtype, device=device)) if bias else None
         self.layer = InstantLayer(make_config(L, Cx, Cy, B_max, R_max=R_max, p=p, N_t=N_t, eps=eps,

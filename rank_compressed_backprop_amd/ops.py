@@ -330,6 +330,18 @@ def differentiated_once(backward):
     return checked
 
 
+def weight_parameter(weight, device, dtype) -> torch.nn.Parameter:
+    """A layer's weight from the one that its caller hands over. A Parameter of this device and type,
+    contiguous, is taken as it is: handed to two layers, it is one leaf with one gradient. Anything
+    else is copied: no two Parameters share memory, which would each get a part of the gradient and
+    an optimizer would step twice."""
+    if (isinstance(weight, torch.nn.Parameter) and weight.dtype == dtype and weight.is_contiguous()
+            and weight.device == torch.empty(0, device=device).device):
+        return weight
+    return torch.nn.Parameter(weight.detach().to(device=device, dtype=dtype, copy=True,
+                                                 memory_format=torch.contiguous_format))
+
+
 # ----------------------------------------------------------------------------- checkpoints
 
 class Checkpoint8(NamedTuple):

@@ -809,3 +809,34 @@ def test_a_training_step(tied):
     for p, got, r in zip(ps, grads, ref):
         assert (got.double() - r).norm() <= 3e-5 * r.norm() + 1e-9, tuple(p.shape)
         assert (p.grad.double() - r * 0.1 / (total + 1e-6)).norm() <= 4e-5 * r.norm() * 0.1 / total + 1e-9
+
+
+@pytest.mark.parametrize("given", ["parameter", "layer"])
+def test_a_tied_step_through_the_constructors(given):
+    """One Parameter handed to both ends, or one end's weight to the other: one leaf with the sum of
+    both gradients, one norm, one step of the optimizer. (float32 sums of at most 192 terms: 1e-5.)"""
+    from rank_compressed_backprop_amd.clip import clip_grad_norm_
+    from rank_compressed_backprop_amd.embedding import InstantEmbedding
+    from rank_compressed_backprop_amd.linear import InstantLinear
+    from rank_compressed_backprop_amd.loss import token_logprobs
+    print(f"[tied] {given}", flush=True)
+    g = gen("tied", given)
+    B, L, C, V = 2, 64, 64, 192
+    w = torch.nn.Parameter(randn(g, V, C, sd=0.3))
+    emb = InstantEmbedding(V, C, scale=2.0, dtype="fp32", weight=w if given == "parameter" else w.detach())
+    head = InstantLinear(L, C, V, B, N_t=4, N_cal=2, dtype="fp32", weight=w if given == "parameter" else emb.weight,
+                         bias=True)
+    assert head.weight is emb.weight and (emb.weight is w) == (given == "parameter")
+    t = torch.randint(0, V, (B, L), generator=g).cuda()
+    want = torch.randint(0, V, (B, L), generator=g).cuda()
+    (-token_logprobs(head(emb(t)), want).logp.mean()).backward()
+    d = w.detach().double().requires_grad_(True)
+    lp = (2 * d[t] @ d.t()).log_softmax(-1).gather(-1, want[..., None])
+    (ref,) = torch.autograd.grad(-lp.mean(), d)
+    assert (emb.weight.grad.double() - ref).norm() <= 1e-5 * ref.norm()
+    ps = [emb.weight, head.weight]
+    norm = clip_grad_norm_(ps, 0.01)
+    assert abs(norm.double() - ref.norm()) <= 1e-5 * ref.norm()
+    before, step = emb.weight.detach().clone(), emb.weight.grad.clone()
+    torch.optim.SGD({id(p): p for p in ps}.values(), lr=0.5).step()
+    assert torch.equal(emb.weight.detach(), torch.add(before, step, alpha=-0.5))

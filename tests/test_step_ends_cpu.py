@@ -167,3 +167,51 @@ def test_second_derivatives_are_refused(monkeypatch):
         for loss in (call().square().sum(), call().sum()):
             with pytest.raises(RuntimeError, match="differentiated again"):
                 torch.autograd.grad(loss, leaf, create_graph=True)
+
+
+@pytest.fixture
+def layers(monkeypatch):
+    """(make, rows, columns) of the layers that take a weight, without a GPU."""
+    from rank_compressed_backprop_amd import embedding, linear
+    monkeypatch.setattr(linear, "InstantLayer", lambda *a, **k: None)
+    return [lambda w, **k: embedding.InstantEmbedding(50, 16, dtype="fp32", weight=w, device="cpu", **k),
+            lambda w, **k: linear.InstantLinear(8, 16, 50, 2, dtype="fp32", weight=w, device="cpu", **k)]
+
+
+def test_a_parameter_is_tied_by_the_constructors(layers):
+    """One Parameter handed to both layers is one leaf, with one gradient that both add to."""
+    w = torch.nn.Parameter(torch.randn(50, 16))
+    made = [make(w) for make in layers]
+    assert all(m.weight is w for m in made)
+    assert len({id(p) for m in made for p in m.parameters()}) == 1
+    (made[0].weight.sum() + 2 * made[1].weight.sum()).backward()
+    assert torch.equal(w.grad, torch.full_like(w, 3.0))
+    for make, first in zip(layers, reversed(layers)):  # one layer's weight handed to the other
+        made = first(None)
+        assert make(made.weight).weight is made.weight
+    frozen = torch.nn.Parameter(torch.randn(50, 16), requires_grad=False)
+    assert all(make(frozen).weight is frozen for make in layers)
+
+
+def test_two_parameters_never_share_memory(layers):
+    """What is not a Parameter of the layer's type, device and layout is copied."""
+    base = torch.randn(50, 16)
+    others = [base, base.clone().requires_grad_(True), base.bfloat16(), torch.nn.Parameter(base.double()),
+              torch.nn.Parameter(base.t().contiguous().t()), torch.randn(100, 16)[::2], torch.randn(60, 16)[5:55]]
+    for make in layers:
+        for w in others:
+            before = w.detach().clone()
+            made = make(w).weight
+            assert isinstance(made, torch.nn.Parameter) and made.requires_grad and made.is_leaf
+            assert made.is_contiguous() and made.dtype == torch.float32 and torch.equal(made, before.float())
+            assert made.untyped_storage().data_ptr() != w.untyped_storage().data_ptr()
+            assert made.untyped_storage().nbytes() == 50 * 16 * 4
+            with torch.no_grad():
+                made.zero_()
+            assert torch.equal(w.detach(), before)
+
+
+def test_padding_row_of_a_given_weight(layers):
+    """Zeros stand in the padding token's row of a weight that the layer makes; a given one is kept."""
+    w = torch.nn.Parameter(torch.ones(50, 16))
+    assert layers[0](w, padding=3).weight[3].all() and not layers[0](None, padding=3).weight[3].any()
