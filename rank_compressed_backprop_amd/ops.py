@@ -282,6 +282,10 @@ def _finite(v, name):
         raise ValueError(f"{name} must be a finite float32, got {v}")
 
 
+# A kernel writes through an address, which autograd does not see: a call that writes a tensor of
+# its caller's says so, and a backward pass that has saved it raises instead of using what it holds now.
+_written = torch.autograd.graph.increment_version
+
 # Sizes depend on the shapes alone.
 _fwd_bytes = functools.lru_cache(4096)(instant_linear_fwd_workspace_bytes)
 _gx_bytes = functools.lru_cache(4096)(instant_linear_gx_workspace_bytes)
@@ -615,6 +619,8 @@ def embedding_backward(gy, tokens, vocab, scale=1.0, padding=None, into=None):
     ws, wp = _workspace(n, gy)
     _ok(_lib.instant_embed_bwd(gy.data_ptr(), tokens.data_ptr(), size, M, vocab, C, dt, scale, padding,
                                into is not None, gw.data_ptr(), wp, n, _current(dev)), "instant_embed_bwd")
+    if into is not None:
+        _written(into)
     return gw
 
 
@@ -710,14 +716,16 @@ def token_logprobs_backward(logits, targets, stats, g_logp=None, g_lse=None, g_e
     _ok(_lib.instant_logprobs_bwd(logits.data_ptr(), _p(targets), size, M, W, V, dt, ignore, stats.data_ptr(),
                                   _p(entropy), _p(g_logp), _p(g_lse), _p(g_entropy), gz.data_ptr(), _current(dev)),
         "instant_logprobs_bwd")
+    if in_place:
+        _written(logits)
     return gz
 
 
 # ----------------------------------------------------------------------------- gradients of a model
 
 def _grads(tensors, name):
-    """Of a sequence of tensors: the first, and of each the address, the elements and the dtype code (a
-    model has hundreds: each question is put to all of them at once)."""
+    """Of a sequence of tensors: a list of them, and of each the address, the elements and the dtype code
+    (a model has hundreds: each question is put to all of them at once)."""
     if isinstance(tensors, Tensor):
         raise TypeError(f"{name} must be a sequence of tensors, got a tensor")
     tensors = list(tensors)
@@ -734,14 +742,14 @@ def _grads(tensors, name):
         raise ValueError(f"{name} must be on the current CUDA device, got {[str(t.device) for t in tensors]}")
     if not all(map(Tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    return tensors[0], list(map(Tensor.data_ptr, tensors)), list(map(Tensor.numel, tensors)), codes
+    return tensors, list(map(Tensor.data_ptr, tensors)), list(map(Tensor.numel, tensors)), codes
 
 
 def grad_norm(tensors) -> torch.Tensor:
     """The Euclidean norm over all elements of a sequence of tensors (float32 and bfloat16 in any
     mixture, of any shapes), a float32 scalar on the device. Squares are summed in float64."""
-    first, at, count, codes = _grads(tensors, "tensors")
-    n = len(at)
+    tensors, at, count, codes = _grads(tensors, "tensors")
+    first, n = tensors[0], len(at)
     norm = first.new_empty((), dtype=torch.float32)
     size = _grads_bytes(n)
     ws, wp = _workspace(size, first)
@@ -757,13 +765,13 @@ def clip_grads(tensors, max_norm, out=None) -> torch.Tensor:
     float32 scalar on the device; nothing waits for it). out: as many tensors of as many elements each,
     float32 or bfloat16, that receive the result; None: the tensors themselves. Outputs may not share memory
     with each other or with another tensor of the call."""
-    first, at, count, codes = _grads(tensors, "tensors")
+    tensors, at, count, codes = _grads(tensors, "tensors")
     if not max_norm >= 0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
-    n = len(at)
+    first, n = tensors[0], len(at)
     to, to_codes = at, codes
     if out is not None:
-        _, to, to_count, to_codes = _grads(out, "out")
+        out, to, to_count, to_codes = _grads(out, "out")
         if to_count != count:
             raise ValueError(f"out must hold tensors of {count} elements, got {to_count}")
     norm = first.new_empty((), dtype=torch.float32)
@@ -772,4 +780,5 @@ def clip_grads(tensors, max_norm, out=None) -> torch.Tensor:
     g, c, d, o, e = _Host("Q", at), _Host("q", count), _Host("i", codes), _Host("Q", to), _Host("i", to_codes)
     _ok(_lib.instant_clip_grads(g.at, c.at, d.at, o.at, e.at, n, max_norm, norm.data_ptr(), wp, size,
                                 _current(first.get_device())), "instant_clip_grads")
+    _written(tensors if out is None else out)
     return norm

@@ -840,3 +840,54 @@ def test_a_tied_step_through_the_constructors(given):
     before, step = emb.weight.detach().clone(), emb.weight.grad.clone()
     torch.optim.SGD({id(p): p for p in ps}.values(), lr=0.5).step()
     assert torch.equal(emb.weight.detach(), torch.add(before, step, alpha=-0.5))
+
+
+def test_autograd_sees_what_is_written_in_place():
+    """A backward pass that has saved what a call overwrote raises, as with torch's own in-place
+    operations; a tensor that is only read, or whose call is refused, stays as it was."""
+    from rank_compressed_backprop_amd import ops
+    from rank_compressed_backprop_amd.clip import clip_grad_norm_
+    from rank_compressed_backprop_amd.loss import token_logprobs
+    g = gen("version")
+    t = torch.arange(4).cuda()
+    z = randn(g, 4, 16).requires_grad_(True) * 2
+    out = token_logprobs(z, t)
+    ops.token_logprobs_backward(z, t, out.stats, torch.ones(4, device="cuda"))
+    out.logp.sum().backward(retain_graph=True)  # nothing was written
+    ops.token_logprobs_backward(z, t, out.stats, torch.ones(4, device="cuda"), in_place=True)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        out.logp.sum().backward()
+
+    def saved(write, read=None):
+        """Whether a product that has saved buf refuses its backward pass after write(buf)."""
+        buf, w = randn(g, 4, 16), torch.ones(4, 16, device="cuda", requires_grad=True)
+        loss = (w * buf).sum()
+        write(buf)
+        try:
+            loss.backward()
+        except RuntimeError as e:
+            assert "inplace operation" in str(e)
+            return True
+        assert torch.equal(w.grad, buf)
+        return False
+
+    def by_parameter(buf):
+        p = torch.nn.Parameter(torch.zeros_like(buf))
+        p.grad = buf
+        clip_grad_norm_(p, 0.1)
+
+    def refused(buf):
+        with pytest.raises(ops.InstantError):
+            ops.clip_grads([buf, buf], 0.1)
+    other = randn(g, 4, 16)
+    for write in (lambda b: ops.embedding_backward(other, t, 4, into=b), lambda b: ops.clip_grads([b], 0.1),
+                  lambda b: ops.clip_grads([other], 0.1, [b]), lambda b: ops.clip_grads([other, b[1], b[2:]], 0.1),
+                  by_parameter):
+        assert saved(write)
+    for write in (lambda b: ops.embedding_backward(b, t, 4, into=other), lambda b: ops.grad_norm([b]), refused,
+                  lambda b: ops.clip_grads([b], 0.1, [other]), lambda b: ops.embedding_backward(b, t, 4)):
+        assert not saved(write)
+    with torch.inference_mode():  # (tensors without a version)
+        b = randn(g, 4, 16)
+        assert ops.clip_grads([b], 0.1) > 0 and b.norm() <= 0.1001
+        ops.embedding_backward(b, t, 4, into=b * 0)
