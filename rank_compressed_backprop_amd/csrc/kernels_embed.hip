@@ -80,8 +80,20 @@ __device__ __forceinline__ uint64_t lanes_like(unsigned v, int bits, uint64_t in
   return m;
 }
 
+// What this lane has written to LDS is there for the wave's other lanes, and what it reads from here on
+// is what they have written. (A wave's LDS operations run in order: no wait is needed, but neither the
+// compiler nor the lanes' lock step promises the order without this.)
+__device__ __forceinline__ void wave_settled() {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+#endif
+}
+
 // Adds the lanes of `in` (this one too if `is`) to counts[v]; returns this lane's number among
-// those with its v, the wave's earlier ones first. Nothing is atomic: counts are the wave's own.
+// those with its v, the wave's earlier ones first. Nothing is atomic: counts are the wave's own, and
+// what one call's lanes have added is settled before the next call's (other) lanes read it.
 __device__ __forceinline__ int number_in(int* counts, unsigned v, int bits, uint64_t in, bool is, int lane) {
   const uint64_t like = lanes_like(v, bits, in);
   const int before = __popcll(like & ((1ull << lane) - 1)), leader = __ffsll((unsigned long long)like) - 1;
@@ -90,6 +102,7 @@ __device__ __forceinline__ int number_in(int* counts, unsigned v, int bits, uint
     base = counts[v];
     counts[v] = base + __popcll(like);
   }
+  wave_settled();
   return __shfl(base, leader < 0 ? 0 : leader) + before;
 }
 
