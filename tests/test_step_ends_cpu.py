@@ -215,3 +215,11 @@ def test_padding_row_of_a_given_weight(layers):
     """Zeros stand in the padding token's row of a weight that the layer makes; a given one is kept."""
     w = torch.nn.Parameter(torch.ones(50, 16))
     assert layers[0](w, padding=3).weight[3].all() and not layers[0](None, padding=3).weight[3].any()
+
+
+def test_gradient_that_overlaps_its_logits():
+    """In place is the same address; any other overlap is refused, also where both are aligned."""
+    for d in (16, 32, 64, 784, 796, 798):  # (4 rows of 100 in bfloat16 are 800 bytes)
+        assert lp_bwd(z=FAR, gz=FAR + d) == E_ARG and lp_bwd(z=FAR + d, gz=FAR) == E_ARG, d
+    for d in (4, 800, 1596):
+        assert lp_bwd(z=FAR, gz=FAR + d, dtype=FP) == E_ARG and lp_bwd(z=FAR + d, gz=FAR, dtype=FP) == E_ARG, d
