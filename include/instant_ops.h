@@ -149,8 +149,11 @@ instant_status instant_embed_fwd(const void* tokens, int32_t token_bytes, int32_
 size_t instant_embed_workspace_bytes(int32_t M, int32_t V, int32_t C);
 
 /* The table's gradient: gtable[v] = scale * sum of the rows of gy [M, C] whose token is v, added in
- * float32 in the order of the rows; rows without a token are zeros. Rows whose token is `padding`
- * (-1: none) take no part. accumulate != 0: the sums are added to what gtable holds (and rounded
+ * float32; rows without a token are zeros. The tokens alone fix the order of the additions, so the bits
+ * are the same every time. It is not row after row: the rows, grouped by token (a token's in their order),
+ * are added in eights, those in tiles of 64 and those by eighths of a run, and where a run is cut depends
+ * on how many rows other tokens have before it. Rows whose token is `padding` (-1: none) take no part.
+ * accumulate != 0: the sums are added to what gtable holds (and rounded
  * once), rows without a token stay as they are. gtable may not share memory with gy (E_ARG). M <= 2^22,
  * M * C <= 2^36. */
 instant_status instant_embed_bwd(const void* gy, const void* tokens, int32_t token_bytes, int32_t M, int32_t V,
@@ -182,7 +185,8 @@ instant_status instant_logprobs_fwd(const void* logits, const void* targets, int
  * all) of logp, lse and entropy, with stats and (for g_entropy) entropy from the forward pass:
  *   gz_j = g_logp (1[j = t] - p_j) + g_lse p_j - g_entropy p_j (log p_j + entropy),   j < V
  * and 0 in the columns behind V. g_logp needs targets, and takes no part where they are `ignore`.
- * A row whose gradients are all 0 gets zeros, whatever it holds. gz may be logits itself,
+ * A row whose gradients are all 0 gets zeros, whatever it holds (with g_logp, unless its target is outside
+ * the vocabulary: NaN). gz may be logits itself,
  * but not share memory with it otherwise (E_ARG). */
 instant_status instant_logprobs_bwd(const void* logits, const void* targets, int32_t token_bytes, int32_t M,
                                     int32_t W, int32_t V, int32_t dtype, int64_t ignore, const float* stats,

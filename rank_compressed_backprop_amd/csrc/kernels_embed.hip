@@ -1,8 +1,9 @@
 // Rows of a table looked up by token and scaled, and the table's gradient (include/instant_ops.h):
-//   y[m] = s W[t[m]]        gW[v] = s sum_{m: t[m] = v} gy[m], in the order of m
+//   y[m] = s W[t[m]]        gW[v] = s sum_{m: t[m] = v} gy[m]
 //
-// The gradient groups the places of equal tokens and sums their rows, so it needs no float atomics
-// and gives the same bits every time:
+// The gradient groups the places of equal tokens, in their order, and sums their rows in eights, the
+// eights of a tile of 64 and the tiles of a run by its eighths, so it needs no float atomics and gives the same bits
+// every time (the order is the tokens' alone, but not one row after the other):
 //   split      segments of 1024 tokens, each ordered by class (token mod CLASSES, so that frequent
 //              tokens, which often have low numbers, are spread)
 //   group      a block a class collects its tokens from the segments and orders them by token; it

@@ -260,8 +260,8 @@ __device__ __forceinline__ Target target_of(const T* row, const void* targets, b
 // cache), and the elements that reach it, a few more than k too, are ranked by counting.
 // Should more reach it than are held, the k-th of those held is a higher bound, and they are looked up
 // again (each time at least as many fewer reach it as are held, but k).
-// (16384 x 30522, k = 20, takes 251 us against 195 for k = 0 or 1, back to back: what follows a row's pass
-// keeps its registers from the next row. A block of 256 threads a row, with its barriers, took 310;
+// (16384 x 30522, back to back, takes 196 to 204 us with k = 0, 218 with 1 and 243 to 251 with 20: what follows
+// a row's pass keeps its registers from the next row. A block of 256 threads a row, with its barriers, took 310;
 // reading again all chunks of the threads whose best reaches the bound 364, holding such chunks in LDS
 // during the pass 360.)
 template <class T, int TPR, int TOP, bool SPLIT>

@@ -29,8 +29,8 @@ class InstantEmbedding(torch.nn.Module):
     weight is given). weight: where the weight starts. A Parameter of the layer's type and device,
     contiguous, is taken as it is, so it may also be the last product's (tied): hand one Parameter,
     or one layer's weight, to both constructors, and autograd adds the gradients. Anything else is
-    copied, and not tied. The gradient is dense [V, C], has the same bits every time, and cannot be
-    differentiated again (create_graph=True raises RuntimeError)."""
+    copied, and not tied. The gradient is dense [V, C], takes at most 2^22 tokens, has the same bits
+    every time, and cannot be differentiated again (create_graph=True raises RuntimeError)."""
 
     def __init__(self, V, C, scale=1.0, padding=None, dtype="bf16", weight=None, device="cuda"):
         super().__init__()

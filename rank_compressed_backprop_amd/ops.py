@@ -598,7 +598,7 @@ def _vocab(V, name):
 
 def embedding_backward(gy, tokens, vocab, scale=1.0, padding=None, into=None):
     """The table's gradient [vocab, C]: scale * the sums of gy's rows [..., C] by their tokens
-    [...], in the order of the rows; rows of the token `padding` take no part, nor does a token
+    [...], with the same bits every time; rows of the token `padding` take no part, nor does a token
     outside the vocabulary. into: a gradient [vocab, C] that the sums are added to, in place (rows
     without a token are not touched), and which is returned. At most 2^22 tokens."""
     M, C, dt = _matrix(gy, "gy")
@@ -696,8 +696,9 @@ def token_logprobs_backward(logits, targets, stats, g_logp=None, g_lse=None, g_e
     """The gradient of logits (of their shape and type) for the gradients g_logp, g_lse and
     g_entropy [...] of token_logprobs' results, with its stats and (for g_entropy) its entropy:
     g_logp (1[j = target] - p) + g_lse p - g_entropy p (log p + entropy), zeros behind the
-    vocabulary. A row whose gradients are all 0 gets zeros, whatever it holds. in_place: it is
-    written over logits and logits are returned."""
+    vocabulary. A row whose gradients are all 0 gets zeros, whatever it holds (with g_logp, unless its
+    target is outside the vocabulary: NaN). in_place: it is written over logits and logits are
+    returned; a later backward pass that has saved them raises."""
     M, W, V, dt = _logits(logits, vocab)
     shape, dev = logits.shape[:-1], logits.get_device()
     if g_logp is None and g_lse is None and g_entropy is None:
