@@ -891,3 +891,21 @@ def test_autograd_sees_what_is_written_in_place():
         b = randn(g, 4, 16)
         assert ops.clip_grads([b], 0.1) > 0 and b.norm() <= 0.1001
         ops.embedding_backward(b, t, 4, into=b * 0)
+
+
+def test_logits_gradient_in_place_through_a_product():
+    """Without the loss's layer: the gradient is written over the logits and goes on into the product
+    that made them. (float32 sums of 24 and 40 terms: 1e-5.)"""
+    from rank_compressed_backprop_amd import ops
+    g = gen("through")
+    x, w = randn(g, 40, 24).requires_grad_(True), randn(g, 56, 24).requires_grad_(True)
+    t = torch.randint(0, 56, (40,), generator=g).cuda()
+    z = torch.nn.functional.linear(x, w)
+    out = ops.token_logprobs(z, t)
+    gz = ops.token_logprobs_backward(z, t, out.stats, torch.full((40,), -1 / 40, device="cuda"), in_place=True)
+    assert gz is z
+    z.backward(gz.detach())
+    x64, w64 = (v.detach().double().requires_grad_(True) for v in (x, w))
+    ref = torch.autograd.grad(torch.nn.functional.cross_entropy(x64 @ w64.t(), t), (x64, w64))
+    for got, r in zip((x.grad, w.grad), ref):
+        assert (got.double() - r).norm() <= 1e-5 * r.norm()
