@@ -688,8 +688,11 @@ __global__ __launch_bounds__(256) void logprobs_bwd_kernel(const T* z, const voi
 namespace {
 
 // Slices of a row (1: not split): for few rows of many chunks, a block of 1024 threads for each
-// compute unit, with at most 80 alternatives of a row to join. (64 x 128000 in float32, k = 0 and 20: 20
-// and 27 us in whole rows, 16 and 22 in 4 slices of 256 threads, 14 and 26 in 8.)
+// compute unit, with at most 80 alternatives of a row to join. (Both launches, us, whole rows and 2, 4, 8, 16
+// slices; * the rule's. float32, 128000: 1 row, k = 0 16.9 12.1 9.0 8.1 8.1*, k = 20 24.0 17.3 13.4* 13.1 17.2;
+// 64 rows 19.6 14.7 11.5* 12.4 15.8, k = 20 27.2 19.8 16.8* 23.6 37.3; 128 rows 20.0 15.7* 16.5, 28.2 21.0* 27.3;
+// 256 rows 22.7* 25.4. bfloat16, 32000: 1 row 6.0* 6.9 6.4 6.7, k = 5 9.9* 9.8 9.5 9.5; 64 rows 6.6* 7.8, 10.6*
+// 10.7. Between, whole rows are not the best: 1 row of 65528 8.8* 8.3 7.1 7.0, k = 5 13.5* 11.5 10.2 10.2.)
 int slices_of(bool bf16_io, int M, int V, int k) {
   const int chunks = V / (bf16_io ? 8 : 4);
   if (M > 128 || chunks < 8192) return 1;
